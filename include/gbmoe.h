@@ -455,6 +455,155 @@ moe_status_t moe_profile_enable(int max_calls);
 moe_status_t moe_profile_read(float* stage_ms, const char** stage_names, int max_stages, int* n_stages,
                               int* n_calls);
 
+/*
+ * Operators of a decode step around the layer: rotary positions with the append
+ * to a paged cache, 4-bit linear layers, attention of drafted tokens over the
+ * cache, and the verification of drafted tokens.  The pages have no counterpart
+ * of these entry points; they follow the conventions above.  None of them
+ * allocates or synchronises, and all can be captured in a CUDA graph.  Strides
+ * are in elements; the last dimension of every tensor is contiguous.
+ */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_FP16 1
+#define MOE_DTYPE_FP32 2
+#define MOE_MAX_TREE_NODES 64 /* drafted tokens of one sequence */
+
+/*
+ * Rotary positions.  Pair i of a head at position p turns by p * inv_freq[i]
+ * radians: with c, s = scale * cos, scale * sin of that angle,
+ *   y0 = x0 c - x1 s,  y1 = x1 c + x0 s        (inverse != 0: -s for s)
+ * interleaved == 0: pair i is (rot_offset + i, rot_offset + rot_dim / 2 + i);
+ * interleaved != 0: (rot_offset + 2i, rot_offset + 2i + 1).  Elements outside
+ * [rot_offset, rot_offset + rot_dim) are copied.  Angles are exact to
+ * |p * inv_freq| * 2^-53 radians at any position (64-bit fractions of a turn);
+ * products are fp32, rounded once to the tensors' type.
+ *
+ *   q, k         [tokens, heads, dim] by stride_t and stride_h
+ *   q_out, k_out outputs; either may be its input (in place)
+ *   positions    int32 [tokens], inv_freq fp64 [rot_dim / 2] (device)
+ *   slots        NULL, or int32 [tokens]: the append.  Then k_out is a paged
+ *                cache: the turned keys and the values v (k_heads heads) go to
+ *                page slot / page_size, row slot % page_size of k_out
+ *                (k_page_stride, k_out_stride_t, k_out_stride_h) and v_cache
+ *                (v_page_stride, v_slot_stride, v_head_stride).  Slots outside
+ *                [0, page_size * num_pages) are skipped; the others must differ.
+ * rot_dim is even; dim <= 1024.  16-byte vectors are used where rows, strides and
+ * the ends of the turning part allow, single elements (pairs) otherwise.
+ */
+typedef struct moe_rope_args {
+  int dtype; /* MOE_DTYPE_BF16, _FP16 or _FP32 */
+  int tokens, dim, rot_dim, rot_offset, interleaved, inverse;
+  int q_heads, k_heads; /* either may be 0 */
+  float scale;
+  int page_size, num_pages;
+  const int32_t* positions;
+  const double* inv_freq;
+  const int32_t* slots;
+  const void *q, *k, *v;
+  void *q_out, *k_out, *v_cache;
+  int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h;
+  int64_t q_out_stride_t, q_out_stride_h, k_page_stride, k_out_stride_t, k_out_stride_h;
+  int64_t v_page_stride, v_slot_stride, v_head_stride;
+} moe_rope_args_t;
+moe_status_t moe_rope(const moe_rope_args_t* args, moe_stream_t stream);
+
+/*
+ * Linear layer with 4-bit weights in fused_moe_int4's code format:
+ *   y[m, n] = sum_k x[m, k] * q[n, k] * w_scale[n, k / group]
+ *   x        bf16 or fp16 [M, K] (dtype), row stride x_stride
+ *   w        uint8 [N, K/2]: two's-complement codes, column 2j in the low nibble
+ *            of byte j, column 2j+1 in its high nibble
+ *   w_scale  fp32 [N, K/group], group 32, 64 or 128
+ *   y        as x, [M, N], row stride y_stride
+ * gated != 0: w and w_scale hold 2N rows, gate rows first, and
+ *   y = SiLU(gate) * up.
+ * K is a multiple of group; x rows and w start on 16 bytes.  x is used at its own
+ * precision, sums are fp32, y is rounded once.  Made for the few rows of a
+ * decode step (M up to 64 or so); any M is accepted.
+ */
+moe_status_t moe_linear_int4(int dtype, const void* x, int64_t x_stride, const uint8_t* w, const float* w_scale,
+                             int M, int N, int K, int group, int gated, void* y, int64_t y_stride,
+                             moe_stream_t stream);
+
+/*
+ * Attention of drafted tokens over a paged cache.  Sequence b has
+ * context_lens[b] committed slots and the nodes node_offsets[b] ..
+ * node_offsets[b+1] - 1 (at most MOE_MAX_TREE_NODES), whose keys and values
+ * stand in the slots right after the committed ones.  Node j (counted from the
+ * sequence's first) sees every committed slot and slot context + i for each set
+ * bit i of its tree_mask word:
+ *   out[j, h] = sum_s softmax_s(scale * q[j, h] . K[s, h / g]) V[s, h / g],
+ * g = q_heads / k_heads.  Zeros where it sees nothing.
+ *   q, out       [nodes, q_heads, dim] by stride_t and stride_h, bf16 or fp16
+ *   k_cache, v_cache  [num_pages, page_size, k_heads, dim] by their strides
+ *                (any order of the dimensions), the type of q
+ *   block_table  int32 [batch, table_width] (table_stride): slot s of sequence b
+ *                is row s % page_size of page block_table[b, s / page_size];
+ *                entries past the sequence's end are not read
+ *   context_lens int32 [batch], node_offsets int32 [batch + 1] ascending
+ *   tree_mask    uint64 [nodes], or NULL for chains (node j sees nodes <= j)
+ * All lengths are read on the device, so a captured call serves any of them.
+ * dim is 64 or 128; batch <= 1024; any page_size >= 1.  Strides are multiples of
+ * 8 elements (out: 4), q and the caches 16-byte aligned.  Infinities and NaN in
+ * slots that a node does not see do not reach it.
+ * Checked on the device: pages outside [0, num_pages) are left out; lengths that
+ * do not fit the table are shortened; sequences with bad offsets are left out
+ * (their rows of out are not written).  moe_read_tree_status waits for the
+ * stream and gives the number of sequences with bad lengths or offsets and the
+ * number of bad page reads of the last call on this workspace
+ * (MOE_ERR_BAD_IDS if any).
+ */
+typedef struct moe_tree_attention_args {
+  int dtype; /* MOE_DTYPE_BF16 or _FP16 */
+  int nodes, batch, q_heads, k_heads, dim;
+  int page_size, num_pages, table_width;
+  float scale;
+  int64_t table_stride;
+  const void *q, *k_cache, *v_cache;
+  const int32_t *block_table, *context_lens, *node_offsets;
+  const uint64_t* tree_mask;
+  void* out;
+  int64_t q_stride_t, q_stride_h, out_stride_t, out_stride_h;
+  int64_t k_page_stride, k_slot_stride, k_head_stride, v_page_stride, v_slot_stride, v_head_stride;
+} moe_tree_attention_args_t;
+size_t moe_tree_attention_workspace_size(int nodes, int batch, int q_heads, int k_heads, int dim);
+moe_status_t moe_tree_attention(const moe_tree_attention_args_t* args, void* workspace, size_t workspace_bytes,
+                                moe_stream_t stream);
+moe_status_t moe_read_tree_status(const void* workspace, int32_t status_out[2], moe_stream_t stream);
+
+/*
+ * Verification of drafted tokens from given random numbers.  Sequence b's nodes
+ * are node_offsets[b] .. node_offsets[b+1] - 1 (n <= max_nodes); its target
+ * rows start at node_offsets[b] + b: first the distribution after the committed
+ * tokens, then the one after each node.  A node's coin is the one of its
+ * parent's row.
+ *  - draft_probs given (a chain; parents NULL): node j is kept if the ones before
+ *    it are and coin * draft[j, token] < target[row of j-1, token] (exact).
+ *    After a refusal the next token is a sample of max(target - draft, 0).
+ *  - draft_probs NULL (parents, or NULL for a chain): a node's children share
+ *    [0, 1) in index order, target[token] each; the child whose share holds the
+ *    coin is kept (a repeat of an earlier sibling's token has no share).  If
+ *    none does, the next token is a sample of the row without the children.
+ * After the last kept node the next token is a sample of its row.  A sample of w
+ * is the first x with w_0 + .. + w_x > last_coins[b] * sum(w), sums being exact
+ * in units of 2^-56 (where a residual has no weight: of the target row).
+ *   target_probs fp32 [nodes + batch, vocab], draft_probs fp32 [nodes, vocab]
+ *   tokens, parents int32 [nodes], parents[j] < j counted from the sequence's
+ *                first node, -1 for the committed end
+ *   coins fp32 [nodes + batch], last_coins fp32 [batch], in [0, 1)
+ *   out_tokens   int32 [batch, max_nodes + 1] out: kept tokens, the next, then -1
+ *   path         int32 [batch, max_nodes] out: kept nodes in order, then -1
+ *   accepted     int32 [batch] out: number of kept nodes; -1 (and no tokens) for
+ *                a sequence with bad offsets, tokens or parents, or whose row has
+ *                no weight or a sum above 128
+ * Probabilities above 1 count as 1, negative ones and NaN as 0.
+ */
+moe_status_t moe_verify_draft(const float* target_probs, int64_t target_stride, const float* draft_probs,
+                              int64_t draft_stride, const int32_t* tokens, const int32_t* parents,
+                              const int32_t* node_offsets, const float* coins, const float* last_coins, int batch,
+                              int nodes, int vocab, int max_nodes, int32_t* out_tokens, int32_t* path,
+                              int32_t* accepted, moe_stream_t stream);
+
 /* Static English text for a status code. */
 const char* moe_status_string(moe_status_t status);
 

@@ -249,6 +249,9 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+// SMs of the current device (0 if it cannot be asked).
+int num_sms_current();
+
 // Sets a kernel's dynamic shared memory limit once per device (and size).
 cudaError_t set_smem_limit_once(const void* func, int bytes);
 

@@ -42,7 +42,7 @@ cudaError_t set_smem_limit_once(const void* func, int bytes) {
   return err;
 }
 
-static int num_sms_current() {
+int num_sms_current() {
   static std::mutex mu;
   static int cache[kMaxDevices] = {};
   int dev = 0;

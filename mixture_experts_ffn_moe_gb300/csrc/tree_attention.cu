@@ -1,0 +1,629 @@
+// Attention of drafted tokens over a paged cache: every node of a sequence's draft tree attends to all of the
+// sequence's committed slots and to those drafted slots whose bits its mask has (its ancestors and itself).
+//
+// Mathematics.  For node j and query head h of KV head h / (Hq / Hkv):
+//   out = sum_k softmax_k(scale * q . K_k) V_k  over the visible slots k, in one pass over the cache: a running
+// reference m, the sum l of 2^(s - m) and the unnormalised output are kept in fp32, and partial results over
+// different slots are joined as (m, l, O).  The reference is moved (and O rescaled) only when a row's maximum has
+// grown by more than 2^8; that leaves the result the same and keeps 2^(s - m) at most 2^8.  A row that sees
+// nothing gives zeros.  P is rounded to the cache's type for the product with V (half a step of that type per
+// term, averaging out over the sum, as the output is itself rounded to it).
+//
+// Bound: K and V are read once: 4 * L * Hkv * D bytes.  The nodes of a tree and the query heads of a KV head
+// are rows of one matrix product, so a cache line serves all of them.
+//
+// Work split.  A unit is (sequence, KV head, tile of rows); its cache is cut in tiles of 64 slots.  The tiles of all
+// units form one line that is divided evenly over the CTAs, whatever the lengths; where a unit is cut, the parts
+// go to the workspace as fp32 (m, l, O) and a second kernel joins them in order, so results do not depend on
+// scheduling.  Inside a CTA each warp owns 16 slots of every tile with a ring of cp.async stages of its own, so
+// warps never wait for each other inside a unit.
+#include <cuda_runtime.h>
+
+#include "sm100_ptx.cuh"
+#include "step_ops.cuh"
+
+namespace gbmoe {
+namespace {
+
+constexpr int kAWarps = 4;
+constexpr int kAThreads = kAWarps * 32;
+constexpr int kTile = kAWarps * 16;  // cache slots a tile
+constexpr int kMaxBatch = 1024;
+constexpr int kMaxTreeCtas = 320;    // CTAs that the workspace has room for
+constexpr float kLazy = 8.f;         // growth of a row's maximum (in powers of two) that moves its reference
+
+struct TreeArgs {
+  const void* q;
+  const void* kc;
+  const void* vc;
+  void* out;
+  const int32_t* table;
+  const int32_t* ctx;
+  const int32_t* offs;
+  const unsigned long long* mask;  // null: a chain
+  long long q_t, q_h, o_t, o_h;
+  long long k_page, k_slot, k_head, v_page, v_slot, v_head;
+  long long table_ld;
+  int N, B, Hq, Hkv, pages, table_w;
+  FastDiv page, group;
+  float scale_log2;
+  int32_t* header;    // workspace: [0] CTAs, [1] bad lengths, offsets or counts, then bad pages of every CTA
+  long long* prefix;  // [B + 1] first tile of every sequence, [B + 1] = tiles a CTA
+  float* part_o;      // [CTAs * 2][rows][D]
+  float* part_ml;     // [CTAs * 2][rows][2]
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+__device__ __forceinline__ void ldm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Words of two 16-bit elements: does either hold an infinity or NaN?
+__device__ __forceinline__ bool nonfinite2(__nv_bfloat16, uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ bool nonfinite2(__half, uint32_t w) {
+  return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+}
+
+// Committed slots and nodes of sequence b, brought into range (bad counts what had to be).
+__device__ __forceinline__ void seq_sizes(const TreeArgs& a, int b, int& ctx, int& n, int& bad) {
+  const int lo = a.offs[b], hi = a.offs[b + 1];
+  ctx = a.ctx[b];
+  n = hi - lo;
+  bad = 0;
+  const long long room = static_cast<long long>(a.table_w) * a.page.d;
+  if (lo < 0 || hi < lo || hi > a.N || n > MOE_MAX_TREE_NODES || n > room) { n = 0; bad = 1; }
+  if (ctx < 0) { ctx = 0; bad = 1; }
+  if (ctx > room - n) { ctx = static_cast<int>(room - n); bad = 1; }
+}
+
+// prefix[b] = first tile of sequence b on the line of all tiles; rows = rows of a unit's row tile.
+__device__ __forceinline__ void plan_line(const TreeArgs& a, int rows, long long* prefix, long long* scratch, int* bad) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long base = 0;
+  int nbad = 0;
+  for (int b0 = 0; b0 < a.B; b0 += kAThreads) {
+    const int b = b0 + tid;
+    long long tiles = 0;
+    if (b < a.B) {
+      int ctx, n, bd;
+      seq_sizes(a, b, ctx, n, bd);
+      nbad += bd;
+      if (n > 0) {
+        const int rt = (n * static_cast<int>(a.group.d) + rows - 1) / rows;
+        tiles = static_cast<long long>(a.Hkv) * rt * ((static_cast<long long>(ctx) + n + kTile - 1) / kTile);
+      }
+    }
+    long long incl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    long long before = base, all = 0;
+    for (int w = 0; w < kAWarps; ++w) {
+      if (w < warp) before += scratch[w];
+      all += scratch[w];
+    }
+    if (b < a.B) prefix[b] = before + incl - tiles;
+    base += all;
+    __syncthreads();
+  }
+  if (tid == 0) prefix[a.B] = base;
+  *bad = nbad;
+  __syncthreads();
+}
+
+template <int D> struct TreeCfg {
+  static constexpr int kRow = D * 2;                     // bytes of a cache row
+  static constexpr int kStage = 16 * kRow * 2;           // K and V of 16 slots
+  static constexpr int S = D == 128 ? 3 : 6;             // stages a warp
+  static constexpr int kRing = S * kStage;               // 24 KB a warp
+};
+
+template <int D, int RT> constexpr size_t tree_smem(int B) {
+  return static_cast<size_t>(kAWarps) * (TreeCfg<D>::kRing > RT * 16 * D * 4 ? TreeCfg<D>::kRing : RT * 16 * D * 4) +
+         RT * 16 * D * 2 + (B + 1 + kAWarps) * 8 + kAWarps * (8 * 4 + RT * 16 * 8) + 1024;
+}
+
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
+  using C = TreeCfg<D>;
+  constexpr int R = RT * 16, KS = D / 16, CH = D / 8;  // rows, K steps, 16-byte chunks a row
+  constexpr int kWarpBytes = C::kRing > R * D * 4 ? C::kRing : R * D * 4;
+  extern __shared__ __align__(128) unsigned char smem[];
+  unsigned char* ring = smem + (threadIdx.x >> 5) * kWarpBytes;
+  unsigned char* qs = smem + kAWarps * kWarpBytes;                                       // [R][D]
+  long long* prefix = reinterpret_cast<long long*>(qs + R * D * 2);                      // [B + 1], then scan scratch
+  float* ml = reinterpret_cast<float*>(prefix + a.B + 1 + kAWarps);                      // [warps][R][2]
+  uint32_t* okmask = reinterpret_cast<uint32_t*>(ml + kAWarps * R * 2) + (threadIdx.x >> 5) * 8;  // [S] a warp
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const uint32_t ring_s = sm100::smem_addr(ring), q_s = sm100::smem_addr(qs);
+
+  pdl_trigger();
+  pdl_wait();
+  int bad_plan;
+  plan_line(a, R, prefix, prefix + a.B + 1, &bad_plan);
+  const long long total = prefix[a.B];
+  const long long chunk = (total + gridDim.x - 1) / gridDim.x;
+  if (blockIdx.x == 0) {
+    bad_plan = __syncthreads_count(bad_plan);
+    if (tid == 0) { a.header[0] = gridDim.x; a.header[1] = bad_plan; a.prefix[a.B + 1] = chunk; }
+    for (int b = tid; b <= a.B; b += kAThreads) a.prefix[b] = prefix[b];
+  }
+  int bad_pages = 0;
+  long long pos = blockIdx.x * chunk;
+  const long long end = pos + chunk < total ? pos + chunk : total;
+  while (pos < end) {
+    int b;
+    {
+      int lo = 0, hi = a.B;  // prefix[lo] <= pos < prefix[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= pos) lo = mid; else hi = mid;
+      }
+      b = lo;
+    }
+    int ctx, n, bd;
+    seq_sizes(a, b, ctx, n, bd);
+    const int L = ctx + n, kt = (L + kTile - 1) / kTile;
+    const int rt_n = (n * static_cast<int>(a.group.d) + R - 1) / R;
+    const long long rel = pos - prefix[b];
+    const int unit = static_cast<int>(rel / kt), k0 = static_cast<int>(rel - static_cast<long long>(unit) * kt);
+    const int k1 = static_cast<int>(end - pos < kt - k0 ? k0 + (end - pos) : kt);
+    const int head = unit / rt_n, row0 = (unit - head * rt_n) * R;
+    const int rows = min(R, n * static_cast<int>(a.group.d) - row0), node0 = a.offs[b];
+    const T* kbase = static_cast<const T*>(a.kc) + head * a.k_head;
+    const T* vbase = static_cast<const T*>(a.vc) + head * a.v_head;
+    const int32_t* table = a.table + b * a.table_ld;
+
+    // this warp's 16 slots of tile `it` into stage `st`
+    auto issue = [&](int it, int st) {
+      int page = -1, at = 0;
+      if (lane < 16) {
+        const int slot = it * kTile + warp * 16 + lane;
+        if (slot < L) {
+          const int pi = div_by(slot, a.page);
+          at = slot - pi * a.page.d;
+          page = __ldg(table + pi);
+          if (page < 0 || page >= a.pages) { page = -1; ++bad_pages; }
+        }
+      }
+      const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
+      if (lane == 0) okmask[st] = ok;
+      const uint32_t base = ring_s + st * C::kStage;
+#pragma unroll
+      for (int i = 0; i < 16 * CH / 32; ++i) {
+        const int c = i * 32 + lane, r = c / CH, ch = c % CH;
+        const int pg = __shfl_sync(0xffffffffu, page, r), sl = __shfl_sync(0xffffffffu, at, r);
+        const bool live = pg >= 0;
+        const long long p = live ? pg : 0;
+        const uint32_t dst = base + r * C::kRow + ((ch ^ (r & 7)) << 4);
+        cp_async16(dst, kbase + p * a.k_page + sl * a.k_slot + ch * 8, live);
+        cp_async16(dst + 16 * C::kRow, vbase + p * a.v_page + sl * a.v_slot + ch * 8, live);
+      }
+    };
+    __syncwarp();
+#pragma unroll
+    for (int s = 0; s < C::S - 1; ++s) {
+      if (k0 + s < k1) issue(k0 + s, s);
+      cp_commit();
+    }
+
+    // the unit's rows: row r is node r / group, head r % group of the KV head's queries
+    for (int i = tid; i < R * CH; i += kAThreads) {
+      const int r = i / CH, ch = i % CH;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const int node = div_by(row0 + r, a.group), hq = head * a.group.d + (row0 + r - node * a.group.d);
+        v = ld_v4(static_cast<const T*>(a.q) + (node0 + node) * a.q_t + hq * a.q_h + ch * 8);
+      }
+      *reinterpret_cast<uint4*>(qs + r * C::kRow + ((ch ^ (r & 7)) << 4)) = v;
+    }
+    unsigned long long bits[RT][2];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int row = r * 16 + h * 8 + g;
+        bits[r][h] = 0;
+        if (row < rows) {
+          const int node = div_by(row0 + row, a.group);
+          bits[r][h] = a.mask ? a.mask[node0 + node] : (2ull << node) - 1;
+        }
+      }
+    __syncthreads();
+
+    float o[RT][CH][4], m[RT][2], l[RT][2];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+#pragma unroll
+      for (int d = 0; d < CH; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[r][d][i] = 0.f;
+      m[r][0] = m[r][1] = -INFINITY;
+      l[r][0] = l[r][1] = 0.f;
+    }
+
+    int st = 0;
+    for (int it = k0; it < k1; ++it) {
+      cp_wait<C::S - 2>();
+      __syncwarp();
+      const uint32_t kst = ring_s + st * C::kStage, vst = kst + 16 * C::kRow;
+      const uint32_t ok = okmask[st];
+      const int slot0 = it * kTile + warp * 16;
+      float s[RT][2][4];
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[r][i >> 2][i & 3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t kb[4];
+        const int key = ((lane >> 4) << 3) + (lane & 7), ch = ks * 2 + ((lane >> 3) & 1);
+        ldm4(kst + key * C::kRow + ((ch ^ (key & 7)) << 4), kb);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          uint32_t qa[4];
+          const int qr = r * 16 + (lane & 15), qc = ks * 2 + (lane >> 4);
+          ldm4(q_s + qr * C::kRow + ((qc ^ (qr & 7)) << 4), qa);
+          mma_16816(T(), s[r][0], qa, kb[0], kb[1]);
+          mma_16816(T(), s[r][1], qa, kb[2], kb[3]);
+        }
+      }
+      const bool edge = ok != 0xffffu || slot0 + 16 > ctx;
+      uint32_t p[RT][4];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float v[4] = {s[r][0][2 * h], s[r][0][2 * h + 1], s[r][1][2 * h], s[r][1][2 * h + 1]};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] *= a.scale_log2;
+          if (edge) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int key = (i >> 1) * 8 + 2 * t + (i & 1), node = slot0 + key - ctx;
+              const bool sees = ((ok >> key) & 1) && (node < 0 || ((bits[r][h] >> (node & 63)) & 1));
+              if (!sees) v[i] = -INFINITY;
+            }
+          }
+          float mx = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const bool grow = mx > m[r][h] + kLazy || (m[r][h] == -INFINITY && mx > -INFINITY);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float nm = grow ? mx : m[r][h];
+            const float f = grow ? ex2(m[r][h] - nm) : 1.f;  // 0 for the first reference
+            m[r][h] = nm;
+            l[r][h] *= f;
+#pragma unroll
+            for (int d = 0; d < CH; ++d) { o[r][d][2 * h] *= f; o[r][d][2 * h + 1] *= f; }
+          }
+          const float ref = m[r][h] == -INFINITY ? 0.f : m[r][h];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = ex2(v[i] - ref);
+          l[r][h] += (v[0] + v[1]) + (v[2] + v[3]);
+          p[r][h] = Elem<T>::pack(v[0], v[1]);
+          p[r][2 + h] = Elem<T>::pack(v[2], v[3]);
+        }
+      }
+      if (slot0 + 16 > ctx) {
+        // Drafted slots are hidden from some rows: an infinity or NaN of a hidden value would come through as
+        // 0 * inf.  Such slots (rare) are added to the rows that see them one by one and cleared for the rest.
+        uint32_t odd = 0;
+#pragma unroll
+        for (int i = 0; i < 16 * CH / 32; ++i) {
+          const int c = i * 32 + lane, r = c / CH, ch = c % CH;
+          const uint4 v = *reinterpret_cast<const uint4*>(ring + st * C::kStage + 16 * C::kRow + r * C::kRow + (ch << 4));
+          const bool nf = nonfinite2(T(), v.x) || nonfinite2(T(), v.y) || nonfinite2(T(), v.z) || nonfinite2(T(), v.w);
+          if (nf && slot0 + r >= ctx) odd |= 1u << r;
+        }
+        odd = __reduce_or_sync(0xffffffffu, odd);
+        while (odd) {
+          const int key = __ffs(odd) - 1;
+          odd &= odd - 1;
+          const int node = slot0 + key - ctx;
+          unsigned char* vrow = ring + st * C::kStage + 16 * C::kRow + key * C::kRow;
+          const int src = (lane & ~3) | ((key & 7) >> 1);
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t w = __shfl_sync(0xffffffffu, key < 8 ? p[r][h] : p[r][2 + h], src);
+              const float2 pp = Elem<T>::unpack(w);
+              const float pk = (key & 1) ? pp.y : pp.x;
+              if ((bits[r][h] >> node) & 1) {
+#pragma unroll
+                for (int d = 0; d < CH; ++d) {
+                  const float2 vv = Elem<T>::unpack(*reinterpret_cast<const uint32_t*>(vrow + ((d ^ (key & 7)) << 4) + t * 4));
+                  o[r][d][2 * h] += pk * vv.x;
+                  o[r][d][2 * h + 1] += pk * vv.y;
+                }
+              }
+            }
+          __syncwarp();
+          if (lane < CH) *reinterpret_cast<uint4*>(vrow + lane * 16) = make_uint4(0, 0, 0, 0);
+          __syncwarp();
+        }
+      }
+#pragma unroll
+      for (int db = 0; db < KS; ++db) {
+        uint32_t vb[4];
+        const int key = (((lane >> 3) & 1) << 3) + (lane & 7), ch = db * 2 + (lane >> 4);
+        ldm4t(vst + key * C::kRow + ((ch ^ (key & 7)) << 4), vb);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          mma_16816(T(), o[r][2 * db], p[r], vb[0], vb[1]);
+          mma_16816(T(), o[r][2 * db + 1], p[r], vb[2], vb[3]);
+        }
+      }
+      __syncwarp();
+      const int nx = it + C::S - 1;
+      if (nx < k1) issue(nx, st == 0 ? C::S - 1 : st - 1);
+      cp_commit();
+      st = st + 1 == C::S ? 0 : st + 1;
+    }
+    cp_wait<0>();
+    __syncwarp();
+
+    // join the warps' slots: m, l and O of every row
+    float* mine = reinterpret_cast<float*>(ring);  // [R][D]
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float sum = l[r][h];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const int row = r * 16 + h * 8 + g;
+        if (t == 0) { ml[(warp * R + row) * 2] = m[r][h]; ml[(warp * R + row) * 2 + 1] = sum; }
+#pragma unroll
+        for (int d = 0; d < CH; ++d)
+          *reinterpret_cast<float2*>(mine + row * D + ((d * 8 + 2 * t) ^ ((row & 3) << 3))) =
+              make_float2(o[r][d][2 * h], o[r][d][2 * h + 1]);
+      }
+    __syncthreads();
+    const bool whole = k0 == 0 && k1 == kt;
+    const long long slot = static_cast<long long>(blockIdx.x) * 2 + (k0 == 0 ? 1 : 0);
+    for (int i = tid; i < rows * (D / 4); i += kAThreads) {
+      const int row = i / (D / 4), c = (i % (D / 4)) * 4;
+      float mm = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kAWarps; ++w) mm = fmaxf(mm, ml[(w * R + row) * 2]);
+      const float ref = mm == -INFINITY ? 0.f : mm;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kAWarps; ++w) {
+        const float f = ex2(ml[(w * R + row) * 2] - ref);
+        const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * kWarpBytes) + row * D +
+                                                          (c ^ ((row & 3) << 3)));
+        sum += f * ml[(w * R + row) * 2 + 1];
+        acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
+      }
+      if (whole) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int node = div_by(row0 + row, a.group), hq = head * a.group.d + (row0 + row - node * a.group.d);
+        T* dst = static_cast<T*>(a.out) + (node0 + node) * a.o_t + hq * a.o_h + c;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(Elem<T>::pack(acc.x * inv, acc.y * inv), Elem<T>::pack(acc.z * inv, acc.w * inv));
+      } else {
+        *reinterpret_cast<float4*>(a.part_o + (slot * R + row) * D + c) = acc;
+        if (c == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * R + row) * 2) = make_float2(mm, sum);
+      }
+    }
+    __syncthreads();
+    pos += k1 - k0;
+  }
+  bad_pages = __reduce_add_sync(0xffffffffu, bad_pages);
+  __syncthreads();
+  if (lane == 0) okmask[0] = bad_pages;
+  __syncthreads();
+  if (tid == 0) {
+    int all = 0;
+    for (int w = 0; w < kAWarps; ++w) all += okmask[w * 8];
+    a.header[2 + blockIdx.x] = all;
+  }
+}
+
+// Joins the parts of units that were cut; one warp a row (node, query head).
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(128) tree_join_kernel(TreeArgs a) {
+  pdl_trigger();
+  pdl_wait();
+  const long long row_id = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row_id >= static_cast<long long>(a.N) * a.Hq) return;
+  const int i = static_cast<int>(row_id / a.Hq), hq = static_cast<int>(row_id - static_cast<long long>(i) * a.Hq);
+  // the sequence of node i: offsets ascend where they are valid; the checks below leave the rest out
+  int lo = 0, hi = a.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.offs[mid] <= i) lo = mid; else hi = mid;
+  }
+  const int b = lo;
+  int ctx, n, bd;
+  seq_sizes(a, b, ctx, n, bd);
+  const int j = i - a.offs[b];
+  if (j < 0 || j >= n) return;
+  const int group = a.group.d, head = hq / group, r = j * group + (hq - head * group);
+  const int kt = (ctx + n + kTile - 1) / kTile, rt_n = (n * group + R - 1) / R;
+  const long long chunk = a.prefix[a.B + 1];
+  const long long s = a.prefix[b] + (static_cast<long long>(head) * rt_n + r / R) * kt, e = s + kt;
+  const long long c0 = s / chunk, c1 = (e - 1) / chunk;
+  if (c0 == c1) return;
+  const int row = r % R, parts = static_cast<int>(c1 - c0 + 1);
+  auto at = [&](int p) {
+    const long long c = c0 + p;
+    return (c * 2 + (c * chunk > s ? 0 : 1)) * R + row;
+  };
+  float mm = -INFINITY;
+  for (int p = lane; p < parts; p += 32) mm = fmaxf(mm, a.part_ml[at(p) * 2]);
+  mm = warp_max(mm);
+  const float ref = mm == -INFINITY ? 0.f : mm;
+  constexpr int E = D / 32;
+  float acc[E], sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < E; ++k) acc[k] = 0.f;
+#pragma unroll 4
+  for (int p = 0; p < parts; ++p) {
+    const long long x = at(p);
+    const float2 v = *reinterpret_cast<const float2*>(a.part_ml + x * 2);
+    const float f = ex2(v.x - ref);
+    sum += f * v.y;
+#pragma unroll
+    for (int k = 0; k < E; ++k) acc[k] += f * a.part_o[x * D + lane * E + k];
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  T* dst = static_cast<T*>(a.out) + i * a.o_t + hq * a.o_h + lane * E;
+#pragma unroll
+  for (int k = 0; k < E; k += 2) *reinterpret_cast<uint32_t*>(dst + k) = Elem<T>::pack(acc[k] * inv, acc[k + 1] * inv);
+}
+
+struct TreeLayout {
+  size_t header = 0, prefix = 0, ml = 0, o = 0, total = 0;
+};
+TreeLayout tree_layout(int B, int ctas, int rows, int D) {
+  TreeLayout l;
+  size_t at = 0;
+  auto take = [&](size_t n) { const size_t r = at; at = (at + n + 255) / 256 * 256; return r; };
+  l.header = take((2 + static_cast<size_t>(ctas)) * 4);
+  l.prefix = take((static_cast<size_t>(B) + 2) * 8);
+  l.ml = take(static_cast<size_t>(ctas) * 2 * rows * 8);
+  l.o = take(static_cast<size_t>(ctas) * 2 * rows * D * 4);
+  l.total = at;
+  return l;
+}
+
+// Rows of a row tile: by the average tree, so that most units are one row tile.
+int tree_rows(int N, int B, int Hq, int Hkv) {
+  const long long avg = (static_cast<long long>(N) + B - 1) / B * (Hq / Hkv);
+  return avg <= 16 ? 16 : 32;
+}
+
+template <typename T, int D, int RT>
+cudaError_t launch_tree(TreeArgs& a, int ctas, bool may_cut, cudaStream_t s) {
+  const size_t smem = tree_smem<D, RT>(a.B);
+  auto kern = tree_kernel<T, D, RT>;
+  cudaError_t err = set_smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(tree_smem<D, RT>(kMaxBatch)));
+  if (err != cudaSuccess) return err;
+  err = launch_kernel(kern, dim3(ctas), dim3(kAThreads), smem, s, true, a);
+  if (err != cudaSuccess || !may_cut) return err;
+  const long long rows = static_cast<long long>(a.N) * a.Hq;
+  return launch_kernel(tree_join_kernel<T, D, RT * 16>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, s, true, a);
+}
+
+template <typename T>
+cudaError_t launch_tree_typed(TreeArgs& a, int D, int rows, int ctas, bool may_cut, cudaStream_t s) {
+  if (D == 128) return rows == 16 ? launch_tree<T, 128, 1>(a, ctas, may_cut, s) : launch_tree<T, 128, 2>(a, ctas, may_cut, s);
+  return rows == 16 ? launch_tree<T, 64, 1>(a, ctas, may_cut, s) : launch_tree<T, 64, 2>(a, ctas, may_cut, s);
+}
+
+}  // namespace
+}  // namespace gbmoe
+
+extern "C" size_t moe_tree_attention_workspace_size(int nodes, int batch, int q_heads, int k_heads, int dim) {
+  using namespace gbmoe;
+  if (nodes < 0 || batch <= 0 || batch > kMaxBatch || q_heads <= 0 || k_heads <= 0 || q_heads % k_heads ||
+      (dim != 64 && dim != 128))
+    return 0;
+  return tree_layout(batch, kMaxTreeCtas, tree_rows(nodes, batch, q_heads, k_heads), dim).total;
+}
+
+extern "C" moe_status_t moe_tree_attention(const moe_tree_attention_args_t* r, void* workspace, size_t workspace_bytes,
+                                           moe_stream_t stream) {
+  using namespace gbmoe;
+  return guarded("moe_tree_attention", [&]() -> moe_status_t {
+    auto bad = [](const char* m) { return report_error(MOE_ERR_INVALID_ARG, std::string("moe_tree_attention: ") + m); };
+    auto not_built = [](const char* m) { return report_error(MOE_ERR_UNSUPPORTED, std::string("moe_tree_attention: ") + m); };
+    if (!r) return bad("NULL arguments");
+    if (r->dtype != MOE_DTYPE_BF16 && r->dtype != MOE_DTYPE_FP16) return bad("dtype must be bf16 or fp16");
+    if (r->nodes < 0 || r->batch < 0 || r->q_heads <= 0 || r->k_heads <= 0 || r->page_size <= 0 || r->num_pages < 0 ||
+        r->table_width < 0)
+      return bad("sizes must be positive");
+    if (r->q_heads % r->k_heads) return bad("q_heads must be a multiple of k_heads");
+    if (r->dim != 64 && r->dim != 128) return not_built("head dimension must be 64 or 128");
+    if (r->batch > kMaxBatch) return not_built("more than 1024 sequences");
+    if (r->q_heads / r->k_heads > 1024 || r->k_heads > 65536 || r->nodes > (1 << 20))
+      return not_built("problem too large");
+    if (static_cast<long long>(r->table_width) * r->page_size > 0x7fffff00LL)
+      return not_built("more than 2^31 - 256 slots a sequence");
+    if (!(r->scale > -INFINITY && r->scale < INFINITY)) return bad("scale must be finite");
+    if (r->nodes == 0 || r->batch == 0) return MOE_OK;
+    if (!r->q || !r->k_cache || !r->v_cache || !r->block_table || !r->context_lens || !r->node_offsets || !r->out)
+      return bad("NULL pointer");
+    const long long strides[] = {r->q_stride_t, r->q_stride_h, r->k_page_stride, r->k_slot_stride, r->k_head_stride,
+                                 r->v_page_stride, r->v_slot_stride, r->v_head_stride};
+    for (long long s : strides)
+      if (s % 8) return bad("strides must be multiples of 8 elements (16 bytes)");
+    if (r->out_stride_t % 4 || r->out_stride_h % 4) return bad("output strides must be multiples of 4 elements");
+    if (!aligned(r->q, 16) || !aligned(r->k_cache, 16) || !aligned(r->v_cache, 16)) return bad("q and the caches must be 16-byte aligned");
+    if (!aligned(r->out, 8) || !aligned(r->tree_mask, 8)) return bad("out and tree_mask must be 8-byte aligned");
+    const int rows = tree_rows(r->nodes, r->batch, r->q_heads, r->k_heads);
+    const int sms = num_sms_current();
+    if (sms <= 0) return report_error(MOE_ERR_CUDA, "moe_tree_attention: no CUDA device");
+    const TreeLayout l = tree_layout(r->batch, kMaxTreeCtas, rows, r->dim);
+    if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256))
+      return report_error(MOE_ERR_WORKSPACE, "moe_tree_attention: workspace NULL, misaligned or too small");
+    TreeArgs a{};
+    a.q = r->q; a.kc = r->k_cache; a.vc = r->v_cache; a.out = r->out;
+    a.table = r->block_table; a.ctx = r->context_lens; a.offs = r->node_offsets;
+    a.mask = reinterpret_cast<const unsigned long long*>(r->tree_mask);
+    a.q_t = r->q_stride_t; a.q_h = r->q_stride_h; a.o_t = r->out_stride_t; a.o_h = r->out_stride_h;
+    a.k_page = r->k_page_stride; a.k_slot = r->k_slot_stride; a.k_head = r->k_head_stride;
+    a.v_page = r->v_page_stride; a.v_slot = r->v_slot_stride; a.v_head = r->v_head_stride;
+    a.table_ld = r->table_stride;
+    a.N = r->nodes; a.B = r->batch; a.Hq = r->q_heads; a.Hkv = r->k_heads; a.pages = r->num_pages; a.table_w = r->table_width;
+    a.page = fast_div(r->page_size);
+    a.group = fast_div(r->q_heads / r->k_heads);
+    a.scale_log2 = r->scale * 1.4426950408889634f;
+    char* ws = static_cast<char*>(workspace);
+    a.header = reinterpret_cast<int32_t*>(ws + l.header);
+    a.prefix = reinterpret_cast<long long*>(ws + l.prefix);
+    a.part_ml = reinterpret_cast<float*>(ws + l.ml);
+    a.part_o = reinterpret_cast<float*>(ws + l.o);
+    int ctas = 2 * sms;
+    if (ctas > kMaxTreeCtas) ctas = kMaxTreeCtas;
+    // a unit of one tile is never cut
+    const bool may_cut = static_cast<long long>(r->table_width) * r->page_size > kTile;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return launched("moe_tree_attention", r->dtype == MOE_DTYPE_FP16
+                                              ? launch_tree_typed<__half>(a, r->dim, rows, ctas, may_cut, s)
+                                              : launch_tree_typed<__nv_bfloat16>(a, r->dim, rows, ctas, may_cut, s));
+  });
+}
+
+extern "C" moe_status_t moe_read_tree_status(const void* workspace, int32_t status_out[2], moe_stream_t stream) {
+  using namespace gbmoe;
+  return guarded("moe_read_tree_status", [&]() -> moe_status_t {
+    if (!workspace || !status_out) return report_error(MOE_ERR_INVALID_ARG, "moe_read_tree_status: NULL pointer");
+    int32_t host[2 + kMaxTreeCtas];
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t err = cudaMemcpyAsync(host, workspace, sizeof(host), cudaMemcpyDeviceToHost, s);
+    if (err == cudaSuccess) err = cudaStreamSynchronize(s);
+    if (err != cudaSuccess) return launched("moe_read_tree_status", err);
+    int pages = 0;
+    for (int c = 0; c < host[0] && c < kMaxTreeCtas; ++c) pages += host[2 + c];
+    status_out[0] = host[1];
+    status_out[1] = pages;
+    if (host[1] || pages)
+      return report_error(MOE_ERR_BAD_IDS, "moe_read_tree_status: lengths, node offsets or cache pages out of range");
+    return MOE_OK;
+  });
+}

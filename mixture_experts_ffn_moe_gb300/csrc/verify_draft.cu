@@ -1,0 +1,301 @@
+// Verification of drafted tokens against the target's probabilities, from given random numbers.
+//
+// Mathematics.  Row 0 of a sequence's target rows is the distribution after its committed tokens, row 1 + j the
+// one after drafted node j.  Node j was drafted as a child of parent(j); the coin of the parent's row decides it.
+//  * With draft probabilities q (a chain): token x is kept iff coin * q(x) < p(x); the first refused one is
+//    replaced by a sample of max(p - q, 0).  (Speculative sampling; the result is distributed as p.)
+//  * Without (a tree of candidates): the children of a node share [0, 1) in order, p(child) each; the child whose
+//    share holds the node's coin is kept, else the next token is a sample of p without the children.
+// Where all of a path is kept, the next token is a sample of the last row.  A sample is the first token x with
+// sum_{i <= x} w_i > u * sum_i w_i.
+//
+// Arithmetic.  coin * q is exact in 64 bits.  The weights become 56-bit fixed-point integers (p * 2^56 rounded to
+// nearest), so their sums are exact, do not depend on the order of the threads, and the comparison with the
+// threshold is one of integers: FP64 sums would be equally exact but run at a sixtieth of the integer rate here.
+//
+// Bound: the one row (two with q) of the vocabulary that is sampled from; everything else is a gather of at most
+// 64 probabilities.  A cluster of CTAs shares a sequence's row: each sums a contiguous part, the parts meet
+// through distributed shared memory, and the warp whose part holds the threshold reads it once more.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include "step_ops.cuh"
+
+namespace gbmoe {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kVThreads = 512;
+constexpr int kVWarps = kVThreads / 32;
+constexpr int kMaxCluster = 8;
+
+struct VerifyArgs {
+  const float* target;  // [N + B, V], row stride ldt
+  const float* draft;   // [N, V], row stride ldd; null: a tree of candidates
+  long long ldt, ldd;
+  const int32_t* tokens;   // [N]
+  const int32_t* parents;  // [N] or null (chain)
+  const int32_t* offsets;  // [B + 1]
+  const float* coins;      // [N + B]
+  const float* last;       // [B]
+  int32_t* out_tokens;     // [B, max_nodes + 1]
+  int32_t* path;           // [B, max_nodes]
+  int32_t* accepted;       // [B]
+  int N, V, max_nodes;
+};
+
+// p * 2^56 rounded to nearest for p in [0, 1]; larger values count as 1, negative ones and NaN as 0.
+__device__ __forceinline__ uint64_t fixed56(float p) {
+  p = fminf(p > 0.f ? p : 0.f, 1.f);
+  const uint32_t b = __float_as_uint(p);
+  const uint32_t d = 127u - (b >> 23);  // p = m * 2^(-23 - d)
+  const uint64_t m = static_cast<uint64_t>((b & 0x7fffffu) | 0x800000u) << 34;
+  return d > 58 ? 0ull : ((m >> d) + 1) >> 1;
+}
+
+// u * 2^64 (rounded down) for u in [0, 1); what lies outside is brought to the nearest end.
+__device__ __forceinline__ uint64_t fraction64(float u) {
+  const uint32_t b = __float_as_uint(fminf(u > 0.f ? u : 0.f, 0x1.fffffep-1f));
+  const int e = static_cast<int>(b >> 23) - 86;  // u = m * 2^(e - 64)
+  const uint64_t m = e <= -86 ? 0 : (b & 0x7fffffu) | 0x800000u;
+  return e >= 0 ? m << e : (e < -63 ? 0 : m >> -e);
+}
+
+__device__ __forceinline__ uint64_t weight(float p, float q, bool has_q) {
+  const uint64_t a = fixed56(p);
+  if (!has_q) return a;
+  const uint64_t b = fixed56(q);
+  return a > b ? a - b : 0ull;
+}
+
+__device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+struct Shared {
+  int tok[64], par[64];
+  float p[64];
+  unsigned char again[64];
+  unsigned long long taken, okmask;
+  int n, bad, stop, count;
+  uint64_t warp_tot[kVWarps];
+  float warp_f[kVWarps];
+  uint64_t cta_tot[kMaxCluster];
+  float cta_f[kMaxCluster];
+  int found;
+};
+
+__global__ void __launch_bounds__(kVThreads) verify_kernel(VerifyArgs a) {
+  __shared__ Shared sh;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = cluster.num_blocks(), rank = cluster.block_rank();
+  const int b = blockIdx.x / C;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  pdl_wait();
+
+  // ---- the nodes: probabilities of every drafted token, gathered at once
+  const int lo = a.offsets[b], hi = a.offsets[b + 1];
+  const int n = hi - lo;
+  const bool bad_range = lo < 0 || hi < lo || hi > a.N || n > a.max_nodes;
+  if (tid == 0) { sh.bad = bad_range; sh.taken = 0; sh.found = 0x7fffffff; }
+  __syncthreads();
+  const long long row0 = static_cast<long long>(lo) + b;
+  float coin = 0.f, q = 0.f;
+  if (!bad_range && tid < n) {
+    const int tok = a.tokens[lo + tid], par = a.parents ? a.parents[lo + tid] : tid - 1;
+    const bool ok = tok >= 0 && tok < a.V && par >= -1 && par < tid;
+    if (!ok) sh.bad = 1;
+    sh.tok[tid] = tok;
+    sh.par[tid] = par;
+    sh.p[tid] = 0.f;
+    if (ok) {
+      const float p = a.target[(row0 + par + 1) * a.ldt + tok];
+      sh.p[tid] = p > 0.f ? p : 0.f;
+      coin = a.coins[row0 + par + 1];
+      if (a.draft) q = a.draft[(lo + tid) * a.ldd + tok];
+    }
+  }
+  __syncthreads();
+  const bool bad = sh.bad != 0;
+  if (!bad && tid < n) {  // a sibling's repeat has no share of its own
+    bool again = false;
+    for (int j = 0; j < tid; ++j) again = again || (sh.par[j] == sh.par[tid] && sh.tok[j] == sh.tok[tid]);
+    sh.again[tid] = again;
+  }
+  __syncthreads();
+  if (!bad && tid < n) {
+    bool taken;
+    if (a.draft) {
+      taken = static_cast<double>(coin) * static_cast<double>(q) < static_cast<double>(sh.p[tid]);
+    } else {
+      double before = 0.0;
+      for (int j = 0; j < tid; ++j)
+        if (sh.par[j] == sh.par[tid] && !sh.again[j]) before += static_cast<double>(sh.p[j]);
+      const double c = static_cast<double>(coin);
+      taken = !sh.again[tid] && c >= before && c < before + static_cast<double>(sh.p[tid]);
+    }
+    if (taken) atomicOr(&sh.taken, 1ull << tid);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    unsigned long long ok = 0;
+    int stop = -1, count = 0;
+    if (!bad) {
+      const unsigned long long taken = sh.taken;
+      for (int j = 0; j < n; ++j) {
+        const int p = sh.par[j];
+        if (((taken >> j) & 1) && (p < 0 || ((ok >> p) & 1))) { ok |= 1ull << j; stop = j; ++count; }
+      }
+    }
+    sh.okmask = ok;
+    sh.stop = stop;
+    sh.count = count;
+  }
+  __syncthreads();
+  const int stop = sh.stop, count = sh.count;
+
+  // ---- the row that the next token is drawn from
+  const float* prow = a.target + (row0 + stop + 1) * a.ldt;
+  const bool has_q = a.draft && stop + 1 < n;
+  const float* qrow = has_q ? a.draft + (lo + static_cast<long long>(stop) + 1) * a.ldd : nullptr;
+  const int per_warp = ((a.V + C * kVWarps - 1) / (C * kVWarps) + 31) / 32 * 32;
+  const int ws = min(static_cast<long long>(a.V), static_cast<long long>(rank * kVWarps + warp) * per_warp);
+  const int we = min(a.V, ws + per_warp);
+  int next = -1;
+  // children: 1 = the residual (draft's share, or the refused children, taken away), 0 = the plain row where
+  // the residual has no weight left
+  for (int residual = 1; !bad && residual >= 0 && next < 0; --residual) {
+    uint64_t s = 0;
+    float fs = 0.f;
+#pragma unroll 4
+    for (int i = ws + lane; i < we; i += 32) {
+      const float p = prow[i], qq = has_q && residual ? qrow[i] : 0.f;
+      s += weight(p, qq, has_q && residual);
+      fs += p > 0.f ? fminf(p, 1.f) : 0.f;
+    }
+    if (!a.draft && residual)
+      for (int j = lane; j < n; j += 32)
+        if (sh.par[j] == stop && !sh.again[j] && sh.tok[j] >= ws && sh.tok[j] < we) s -= fixed56(sh.p[j]);
+    s = warp_sum64(s);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) fs += __shfl_xor_sync(0xffffffffu, fs, o);
+    if (lane == 0) { sh.warp_tot[warp] = s; sh.warp_f[warp] = fs; }
+    __syncthreads();
+    if (tid < C) {  // this CTA's total into slot `rank` of every CTA of the cluster
+      uint64_t tot = 0;
+      float f = 0.f;
+      for (int w = 0; w < kVWarps; ++w) { tot += sh.warp_tot[w]; f += sh.warp_f[w]; }
+      Shared* other = cluster.map_shared_rank(&sh, tid);
+      other->cta_tot[rank] = tot;
+      other->cta_f[rank] = f;
+    }
+    cluster.sync();
+    uint64_t total = 0, before = 0;
+    float f = 0.f;
+    for (int r = 0; r < C; ++r) {
+      if (r < rank) before += sh.cta_tot[r];
+      total += sh.cta_tot[r];
+      f += sh.cta_f[r];
+    }
+    if (!(f <= 128.f)) break;  // not probabilities: 56 bits would overflow
+    if (total != 0) {
+      for (int w = 0; w < warp; ++w) before += sh.warp_tot[w];
+      // floor(u * total) for u in [0, 1): x is the first token whose running sum is above it
+      const uint64_t level = __umul64hi(fraction64(a.last[b]), total);
+      if (level >= before && level < before + sh.warp_tot[warp]) {  // one warp of the cluster
+        for (int i0 = ws; i0 < we; i0 += 32) {
+          const int i = i0 + lane;
+          uint64_t w = 0;
+          if (i < we) {
+            w = weight(prow[i], has_q && residual ? qrow[i] : 0.f, has_q && residual);
+            if (!a.draft && residual)
+              for (int j = 0; j < n; ++j)
+                if (sh.par[j] == stop && sh.tok[j] == i) w = 0;
+          }
+          uint64_t run = w;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t up = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += up;
+          }
+          const unsigned hit = __ballot_sync(0xffffffffu, before + run > level);
+          if (hit) {
+            if (lane == 0) {
+              const int x = i0 + __ffs(hit) - 1;
+              cluster.map_shared_rank(&sh, 0)->found = x;
+            }
+            break;
+          }
+          before += __shfl_sync(0xffffffffu, run, 31);
+        }
+      }
+    }
+    cluster.sync();  // found has arrived; the sums may be written again
+    if (total != 0) next = 0;
+  }
+  if (rank == 0) {
+    const int x = next < 0 ? -1 : sh.found;
+    const bool fail = bad || x < 0;
+    if (tid == 0) a.accepted[b] = fail ? -1 : count;
+    // accepted nodes in order, then the next token, then -1
+    if (tid <= a.max_nodes) {
+      int node = -1;
+      if (!fail && tid < count) {
+        unsigned long long m = sh.okmask;
+        for (int i = 0; i < tid; ++i) m &= m - 1;
+        node = __ffsll(static_cast<long long>(m)) - 1;
+      }
+      a.out_tokens[static_cast<long long>(b) * (a.max_nodes + 1) + tid] = node >= 0 ? sh.tok[node] : (!fail && tid == count ? x : -1);
+      if (tid < a.max_nodes) a.path[static_cast<long long>(b) * a.max_nodes + tid] = node;
+    }
+  }
+}
+
+}  // namespace
+}  // namespace gbmoe
+
+extern "C" moe_status_t moe_verify_draft(const float* target_probs, int64_t target_stride, const float* draft_probs,
+                                         int64_t draft_stride, const int32_t* tokens, const int32_t* parents,
+                                         const int32_t* node_offsets, const float* coins, const float* last_coins,
+                                         int batch, int nodes, int vocab, int max_nodes, int32_t* out_tokens,
+                                         int32_t* path, int32_t* accepted, moe_stream_t stream) {
+  using namespace gbmoe;
+  return guarded("moe_verify_draft", [&]() -> moe_status_t {
+    auto bad = [](const char* m) { return report_error(MOE_ERR_INVALID_ARG, std::string("moe_verify_draft: ") + m); };
+    if (batch < 0 || nodes < 0 || vocab <= 0 || max_nodes < 0) return bad("sizes must be positive");
+    if (max_nodes > MOE_MAX_TREE_NODES)
+      return report_error(MOE_ERR_UNSUPPORTED, "moe_verify_draft: more than MOE_MAX_TREE_NODES nodes a sequence");
+    if (vocab > (1 << 24) || batch > (1 << 20))
+      return report_error(MOE_ERR_UNSUPPORTED, "moe_verify_draft: problem too large");
+    if (batch == 0) return MOE_OK;
+    if (!target_probs || !node_offsets || !coins || !last_coins || !out_tokens || !accepted || (max_nodes && !path) ||
+        (nodes && !tokens))
+      return bad("NULL pointer");
+    if (draft_probs && parents) return bad("draft probabilities are verified along a chain (no parents)");
+    if (target_stride < vocab || (draft_probs && draft_stride < vocab)) return bad("a row stride is shorter than its row");
+    const VerifyArgs a{target_probs, draft_probs, target_stride, draft_stride, tokens, parents, node_offsets, coins,
+                       last_coins, out_tokens, path, accepted, nodes, vocab, max_nodes};
+    const int sms = num_sms_current();
+    if (sms <= 0) return report_error(MOE_ERR_CUDA, "moe_verify_draft: no CUDA device");
+    int C = 1;
+    while (C < kMaxCluster && 2 * C * batch <= 4 * sms && vocab > 2 * C * kVThreads) C *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(batch) * C);
+    cfg.blockDim = dim3(kVThreads);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return launched("moe_verify_draft", cudaLaunchKernelEx(&cfg, verify_kernel, a));
+  });
+}

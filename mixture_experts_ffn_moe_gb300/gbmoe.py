@@ -7,7 +7,9 @@ There is no fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
+import struct
 
 import torch
 
@@ -29,6 +31,10 @@ MOE_STATIC_SCRATCH_BYTES = 16 << 20
 MOE_GATE_SOFTMAX = 0
 MOE_GATE_SIGMOID_GROUPED = 1
 MOE_GATE_INLINE_TOKENS = 64
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_FP16 = 1
+MOE_DTYPE_FP32 = 2
+MOE_MAX_TREE_NODES = 64
 
 
 class GateConfig(ctypes.Structure):
@@ -49,6 +55,7 @@ class MoEError(RuntimeError):
 _lib = None
 
 _vp, _i, _u, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint, ctypes.c_size_t
+_i64 = ctypes.c_int64
 _SIGS = {
     "moe_align_max_padded": (_sz, [_i, _i, _i, _i]),
     "moe_align_block_size": (_i, [_vp, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp]),
@@ -69,6 +76,12 @@ _SIGS = {
     "moe_selftest_wait_timeout": (_i, [_vp, ctypes.c_longlong, _vp, _vp]),
     "moe_profile_enable": (_i, [_i]),
     "moe_profile_read": (_i, [_vp, _vp, _i, _vp, _vp]),
+    "moe_rope": (_i, [_vp, _vp]),
+    "moe_linear_int4": (_i, [_i, _vp, _i64, _vp, _vp] + [_i] * 5 + [_vp, _i64, _vp]),
+    "moe_tree_attention_workspace_size": (_sz, [_i] * 5),
+    "moe_tree_attention": (_i, [_vp, _vp, _sz, _vp]),
+    "moe_read_tree_status": (_i, [_vp, _vp, _vp]),
+    "moe_verify_draft": (_i, [_vp, _i64, _vp, _i64] + [_vp] * 5 + [_i] * 4 + [_vp] * 4),
     "moe_status_string": (ctypes.c_char_p, [_i]),
     "moe_last_error": (ctypes.c_char_p, []),
 }
@@ -425,3 +438,298 @@ def moe_profile_read(max_stages: int = 8):
                                  max_stages, ctypes.byref(n_st), ctypes.byref(n_calls))
     _check(st, "moe_profile_read")
     return n_calls.value, [(names[i].decode(), float(ms[i])) for i in range(n_st.value)]
+
+
+# ------------------------------------------------------------------ operators of a decode step around the layer
+# The argument structs are packed by `struct` (native sizes and alignment, as the C compiler lays them out).
+_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_FP16, torch.float32: MOE_DTYPE_FP32}
+_ROPE_ARGS = struct.Struct("@9if2i3P3P3P6q5q3q")
+_TREE_ARGS = struct.Struct("@9ifq3P3PPP4q6q")
+
+
+def _raw_stream(t: torch.Tensor) -> int:
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _float_dtype(t: torch.Tensor, name: str, allowed) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    d = _DTYPES.get(t.dtype)
+    if d is None or d not in allowed:
+        raise ValueError(f"{name} has an unsupported type {t.dtype}")
+    return d
+
+
+def _rows3(t: torch.Tensor, dtype, name: str):
+    """(token stride, head stride) of a [tokens, heads, dim] tensor with a contiguous last dimension."""
+    if not t.is_cuda or t.dtype != dtype or t.dim() != 3:
+        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, dim] of type {dtype}")
+    st = t.stride()
+    if st[2] != 1 and t.shape[2] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return st
+
+
+def _pages4(t: torch.Tensor, dtype, name: str):
+    """Strides of a [pages, page_size, heads, dim] cache with a contiguous last dimension (any order of the rest)."""
+    if not t.is_cuda or t.dtype != dtype or t.dim() != 4:
+        raise ValueError(f"{name} must be a CUDA tensor [pages, page_size, heads, dim] of type {dtype}")
+    st = t.stride()
+    if st[3] != 1 and t.shape[3] > 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return st
+
+
+def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, original_positions=0, beta_fast=32.0,
+                     beta_slow=1.0, device="cuda"):
+    """(inv_freq fp64 [rot_dim / 2] on `device`, scale) for moe_rope.
+
+    scaling: "none"; "linear" (positions divided by `factor`); "ntk" (the base raised so that the slowest pair is
+    stretched by `factor`); "yarn" (pairs that turn less than `beta_slow` times in `original_positions` are
+    stretched by `factor`, those that turn more than `beta_fast` times are kept, the ones between are blended
+    linearly in their index, and the result is multiplied by 0.1 ln(factor) + 1).
+    """
+    if rot_dim <= 0 or rot_dim % 2:
+        raise ValueError("rot_dim must be positive and even")
+    if not base > 1.0 or not factor > 0.0 or not math.isfinite(base) or not math.isfinite(factor):
+        raise ValueError("base must be above 1 and factor positive")
+    half, scale = rot_dim // 2, 1.0
+    i = torch.arange(half, dtype=torch.float64)
+    if scaling == "ntk":
+        if rot_dim <= 2:
+            raise ValueError("ntk scaling needs rot_dim above 2")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = torch.pow(torch.tensor(base, dtype=torch.float64), -2.0 * i / rot_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if original_positions <= 0 or not beta_fast > 0.0 or not beta_slow > 0.0:
+            raise ValueError("yarn scaling needs original_positions and positive betas")
+        low, high = (rot_dim * math.log(original_positions / (turns * 2 * math.pi)) / (2 * math.log(base))
+                     for turns in (beta_fast, beta_slow))
+        low, high = max(math.floor(low), 0), min(math.ceil(high), rot_dim - 1)
+        ramp = ((i - low) / max(high - low, 0.001)).clamp(0.0, 1.0)
+        f = f / factor * ramp + f * (1.0 - ramp)
+        if factor > 1.0:
+            scale = 0.1 * math.log(factor) + 1.0
+    elif scaling not in ("none", "ntk"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    return f.to(device), scale
+
+
+def _rope_tables(positions, inv_freq, tokens):
+    if not positions.is_cuda or positions.dtype != torch.int32 or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int32 CUDA tensor")
+    if not inv_freq.is_cuda or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be a contiguous float64 CUDA tensor")
+    if positions.numel() != tokens:
+        raise ValueError("positions must have one entry a token")
+
+
+def moe_rope(q, k, positions, inv_freq, scale=1.0, interleaved=False, inverse=False, offset=0, q_out=None,
+             k_out=None):
+    """Rotary positions of q and k ([tokens, heads, dim], bf16 / fp16 / fp32; k may be None): (q_out, k_out).
+
+    The 2 * len(inv_freq) elements from `offset` on turn by position * inv_freq; the rest is copied.  q_out and
+    k_out may be the inputs (in place).  See include/gbmoe.h.
+    """
+    dt = _float_dtype(q, "q", (0, 1, 2))
+    qs = _rows3(q, q.dtype, "q")
+    T, hq, D = q.shape
+    _rope_tables(positions, inv_freq, T)
+    if q_out is None:
+        q_out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
+    elif q_out.shape != q.shape:
+        raise ValueError("q_out must have the shape of q")
+    qo = _rows3(q_out, q.dtype, "q_out")
+    hk, kp, kop, ks, ko = 0, 0, 0, (0, 0), (0, 0)
+    if k is not None:
+        ks = _rows3(k, q.dtype, "k")
+        hk = k.shape[1]
+        if k.shape[0] != T or k.shape[2] != D:
+            raise ValueError("q and k must have the same tokens and dim")
+        if k_out is None:
+            k_out = torch.empty((T, hk, D), dtype=q.dtype, device=q.device)
+        elif k_out.shape != k.shape:
+            raise ValueError("k_out must have the shape of k")
+        ko = _rows3(k_out, q.dtype, "k_out")
+        kp, kop = k.data_ptr(), k_out.data_ptr()
+    args = _ROPE_ARGS.pack(dt, T, D, 2 * inv_freq.numel(), offset, interleaved, inverse, hq, hk, scale, 0, 0,
+                           positions.data_ptr(), inv_freq.data_ptr(), 0, q.data_ptr(), kp, 0, q_out.data_ptr(), kop,
+                           0, qs[0], qs[1], ks[0], ks[1], 0, 0, qo[0], qo[1], 0, ko[0], ko[1], 0, 0, 0)
+    st = load().moe_rope(args, _raw_stream(q))
+    if st:
+        _check(st, "moe_rope")
+    return q_out, k_out
+
+
+def moe_rope_append(q, k, v, positions, inv_freq, slots, k_cache, v_cache, scale=1.0, interleaved=False,
+                    inverse=False, offset=0, q_out=None):
+    """moe_rope of q and k, with the turned keys and the values written to slots of a paged cache; returns q_out.
+
+    slots int32 [tokens]: page * page_size + row in k_cache / v_cache [pages, page_size, k_heads, dim]; entries
+    outside the cache (such as -1) are skipped.
+    """
+    dt = _float_dtype(q, "q", (0, 1, 2))
+    qs, ks, vs = _rows3(q, q.dtype, "q"), _rows3(k, q.dtype, "k"), _rows3(v, q.dtype, "v")
+    T, hq, D = q.shape
+    hk = k.shape[1]
+    _rope_tables(positions, inv_freq, T)
+    if k.shape[0] != T or k.shape[2] != D or v.shape != k.shape:
+        raise ValueError("q, k and v must have the same tokens and dim, k and v the same heads")
+    kc, vc = _pages4(k_cache, q.dtype, "k_cache"), _pages4(v_cache, q.dtype, "v_cache")
+    if k_cache.shape != v_cache.shape or k_cache.shape[2] != hk or k_cache.shape[3] != D:
+        raise ValueError("k_cache and v_cache must be [pages, page_size, k_heads, dim]")
+    if not slots.is_cuda or slots.dtype != torch.int32 or not slots.is_contiguous() or slots.numel() != T:
+        raise ValueError("slots must be a contiguous int32 CUDA tensor with one entry a token")
+    if q_out is None:
+        q_out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
+    elif q_out.shape != q.shape:
+        raise ValueError("q_out must have the shape of q")
+    qo = _rows3(q_out, q.dtype, "q_out")
+    args = _ROPE_ARGS.pack(dt, T, D, 2 * inv_freq.numel(), offset, interleaved, inverse, hq, hk, scale,
+                           k_cache.shape[1], k_cache.shape[0], positions.data_ptr(), inv_freq.data_ptr(),
+                           slots.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
+                           k_cache.data_ptr(), v_cache.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], qo[0],
+                           qo[1], kc[0], kc[1], kc[2], vc[0], vc[1], vc[2])
+    st = load().moe_rope(args, _raw_stream(q))
+    if st:
+        _check(st, "moe_rope")
+    return q_out
+
+
+def moe_linear_int4(x, w, w_scale, gated=False, out=None):
+    """x [M, K] (bf16 / fp16) times 4-bit weights w uint8 [N, K/2] with w_scale fp32 [N, K/group]: [M, N].
+
+    gated: w holds 2N rows, gate rows first; SiLU(gate) * up of shape [M, N].  See include/gbmoe.h.
+    """
+    dt = _float_dtype(x, "x", (0, 1))
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("x must be [M, K] with contiguous rows")
+    _need(w, torch.uint8, "w")
+    _need(w_scale, torch.float32, "w_scale")
+    M, K = x.shape
+    rows, half = w.shape
+    groups = w_scale.shape[1]
+    if half * 2 != K or w_scale.shape[0] != rows or groups == 0 or K % groups or (gated and rows % 2):
+        raise ValueError("inconsistent shapes")
+    N = rows // 2 if gated else rows
+    if out is None:
+        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
+    elif out.dtype != x.dtype or not out.is_cuda or tuple(out.shape) != (M, N) or (N > 1 and out.stride(1) != 1):
+        raise ValueError("out must be [M, N] of x's type with contiguous rows")
+    st = load().moe_linear_int4(dt, x.data_ptr(), x.stride(0) if M > 1 else K, w.data_ptr(), w_scale.data_ptr(), M, N,
+                                K, K // groups, 1 if gated else 0, out.data_ptr(), out.stride(0) if M > 1 else N,
+                                _raw_stream(x))
+    if st:
+        _check(st, "moe_linear_int4")
+    return out
+
+
+def moe_tree_attention_workspace_size(nodes, batch, q_heads, k_heads, dim) -> int:
+    return int(load().moe_tree_attention_workspace_size(nodes, batch, q_heads, k_heads, dim))
+
+
+def moe_tree_attention(q, k_cache, v_cache, block_table, context_lens, node_offsets, tree_mask=None, scale=None,
+                       out=None, workspace=None):
+    """Attention of drafted tokens q [nodes, q_heads, dim] over a paged cache (see include/gbmoe.h).
+
+    k_cache, v_cache [pages, page_size, k_heads, dim]; block_table int32 [batch, pages of a sequence];
+    context_lens int32 [batch]; node_offsets int32 [batch + 1]; tree_mask int64 / uint64 [nodes] (None: chains);
+    scale defaults to dim ** -0.5.
+    """
+    dt = _float_dtype(q, "q", (0, 1))
+    qs = _rows3(q, q.dtype, "q")
+    N, hq, D = q.shape
+    kc, vc = _pages4(k_cache, q.dtype, "k_cache"), _pages4(v_cache, q.dtype, "v_cache")
+    pages, page, hk, dk = k_cache.shape
+    if k_cache.shape != v_cache.shape or dk != D:
+        raise ValueError("k_cache and v_cache must be [pages, page_size, k_heads, dim]")
+    if not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2:
+        raise ValueError("block_table must be an int32 CUDA tensor [batch, pages of a sequence]")
+    B, width = block_table.shape
+    if width > 1 and block_table.stride(1) != 1:
+        raise ValueError("the rows of block_table must be contiguous")
+    for t, n, name in ((context_lens, B, "context_lens"), (node_offsets, B + 1, "node_offsets")):
+        if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n:
+            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {n} entries")
+    mask = 0
+    if tree_mask is not None:
+        if (not tree_mask.is_cuda or tree_mask.dtype not in (torch.int64, torch.uint64)
+                or not tree_mask.is_contiguous() or tree_mask.numel() != N):
+            raise ValueError("tree_mask must be a contiguous 64-bit CUDA tensor with one word a node")
+        mask = tree_mask.data_ptr()
+    if out is None:
+        out = torch.empty((N, hq, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    os_ = _rows3(out, q.dtype, "out")
+    lib = load()
+    if workspace is None:
+        n = lib.moe_tree_attention_workspace_size(N, B, hq, hk, D) if B else 256
+        if n == 0:
+            raise MoEError(2, "moe_tree_attention_workspace_size", "unsupported sizes")
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    args = _TREE_ARGS.pack(dt, N, B, hq, hk, D, page, pages, width, D ** -0.5 if scale is None else scale,
+                           block_table.stride(0), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                           block_table.data_ptr(), context_lens.data_ptr(), node_offsets.data_ptr(), mask,
+                           out.data_ptr(), qs[0], qs[1], os_[0], os_[1], kc[0], kc[1], kc[2], vc[0], vc[1], vc[2])
+    st = lib.moe_tree_attention(args, workspace.data_ptr(), workspace.numel(), _raw_stream(q))
+    if st:
+        _check(st, "moe_tree_attention")
+    return out
+
+
+def moe_read_tree_status(workspace: torch.Tensor):
+    """(sequences with bad lengths or offsets, bad page reads, status) of the last moe_tree_attention on `workspace`."""
+    buf = (ctypes.c_int32 * 2)()
+    st = load().moe_read_tree_status(_ptr(workspace), ctypes.cast(buf, ctypes.c_void_p), _stream(workspace))
+    return int(buf[0]), int(buf[1]), int(st)
+
+
+def moe_verify_draft(target_probs, tokens, node_offsets, coins, last_coins, max_nodes, parents=None,
+                     draft_probs=None, out_tokens=None, path=None, accepted=None):
+    """Keeps or refuses drafted tokens and draws the next one (see include/gbmoe.h).
+
+    target_probs fp32 [nodes + batch, vocab]; tokens, parents int32 [nodes]; node_offsets int32 [batch + 1];
+    coins fp32 [nodes + batch]; last_coins fp32 [batch]; draft_probs fp32 [nodes, vocab] (chains only).
+    Returns (out_tokens [batch, max_nodes + 1], path [batch, max_nodes], accepted [batch]), int32.
+    """
+    if not target_probs.is_cuda or target_probs.dtype != torch.float32 or target_probs.dim() != 2:
+        raise ValueError("target_probs must be an fp32 CUDA tensor [nodes + batch, vocab]")
+    N, B, V = tokens.numel(), last_coins.numel(), target_probs.shape[1]
+    if target_probs.shape[0] != N + B or (V > 1 and target_probs.stride(1) != 1):
+        raise ValueError("target_probs must be [nodes + batch, vocab] with contiguous rows")
+    for t, n, dtype, name in ((tokens, N, torch.int32, "tokens"), (node_offsets, B + 1, torch.int32, "node_offsets"),
+                              (coins, N + B, torch.float32, "coins"), (last_coins, B, torch.float32, "last_coins")):
+        if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or t.numel() != n:
+            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {n} entries")
+    pp = dp = ds = 0
+    if parents is not None:
+        if not parents.is_cuda or parents.dtype != torch.int32 or not parents.is_contiguous() or parents.numel() != N:
+            raise ValueError("parents must be a contiguous int32 CUDA tensor with one entry a node")
+        pp = parents.data_ptr()
+    if draft_probs is not None:
+        if (not draft_probs.is_cuda or draft_probs.dtype != torch.float32 or tuple(draft_probs.shape) != (N, V)
+                or (V > 1 and draft_probs.stride(1) != 1)):
+            raise ValueError("draft_probs must be an fp32 CUDA tensor [nodes, vocab] with contiguous rows")
+        dp, ds = draft_probs.data_ptr(), max(draft_probs.stride(0), V)
+    dev = target_probs.device
+    for name, t, shape in (("out_tokens", out_tokens, (B, max_nodes + 1)), ("path", path, (B, max_nodes)),
+                           ("accepted", accepted, (B,))):
+        if t is not None:
+            _need(t, torch.int32, name)
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+    if out_tokens is None:
+        out_tokens = torch.empty((B, max_nodes + 1), dtype=torch.int32, device=dev)
+    if path is None:
+        path = torch.empty((B, max_nodes), dtype=torch.int32, device=dev)
+    if accepted is None:
+        accepted = torch.empty(B, dtype=torch.int32, device=dev)
+    st = load().moe_verify_draft(target_probs.data_ptr(), max(target_probs.stride(0), V), dp, ds, tokens.data_ptr(), pp,
+                                 node_offsets.data_ptr(), coins.data_ptr(), last_coins.data_ptr(), B, N, V, max_nodes,
+                                 out_tokens.data_ptr(), path.data_ptr(), accepted.data_ptr(), _raw_stream(target_probs))
+    if st:
+        _check(st, "moe_verify_draft")
+    return out_tokens, path, accepted
