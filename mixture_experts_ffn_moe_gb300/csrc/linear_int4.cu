@@ -2,22 +2,40 @@
 // gated form y = SiLU(gate) * up of two such products, for the few rows of a decode step.
 //
 // Every weight is read once, so HBM bounds the product: N * K / 2 bytes of codes and 4 bytes a group of
-// scales.  A warp owns 16 weight rows and walks over K in blocks of 128; each lane loads 16 bytes (32 codes)
-// of two rows straight into registers, several blocks ahead, so nothing waits on a barrier.  The codes
-// become exact 16-bit floats (bf16 or fp16, the type of x) and enter m16n8k16 tensor-core products as the
-// 16-row operand with up to 8 tokens as columns; the K order inside a block is the same permutation for both
-// operands.  Products are exact and summed in fp32; each group's sum is scaled by its row's scale in fp32,
-// and the only rounding to 16 bits is the one of y.  The warps of a CTA split K and meet in shared memory in
-// a fixed order, so results do not depend on scheduling.
+// scales.  A warp owns 32 weight rows (16 where that spreads better) and a share of K in blocks of 128; each
+// lane loads 16 bytes (32 codes) of each of its rows straight into registers, blocks ahead of their use and
+// across tiles, so the weight stream waits on no barrier.  The codes become fp16 and enter m16n8k16 tensor-core
+// products as the 16-row operand with 8 tokens as columns.
+//
+// x is brought into the order in which the products take it: per block and 8 tokens four 16-byte pieces a lane,
+// each 8 values paired (k0,k4) (k1,k5) (k2,k6) (k3,k7) as the codes come out of their words.  Like the layer's
+// weight-only paths it is kept as fp16 in power-of-two frames, one per token and block: the block's largest |x|
+// lies in [2^14, 2^15), so what fp16 rounds off is below 2^-39 of it, far below the fp32 sums.
+//  * Up to 8 tokens whose x fits: every CTA (persistent, one an SM) does that itself into shared memory, where x
+//    stays for all of its tiles: one launch.
+//  * Otherwise a first kernel writes the pieces to the workspace, and each warp brings those of its next blocks
+//    into a cp.async ring of its own (a lane reads back what it fetched): no barriers and any M and K.
+//
+// Expansion.  It is the integer pipe that limits this kernel beside HBM, so a pair of codes takes one LOP3 (and a
+// word one shift): the biased code u = q + 8 stands alone in an fp16 as a subnormal, u * 2^-24, or 16 u * 2^-24
+// where its nibble is the higher one; the tensor cores take subnormals exactly, and the pieces (k1,k5), (k3,k7)
+// of x are stored divided by 16.  sum x u = sum x q + 8 sum x, so the accumulators of a group start at -8 times
+// the group's sum of x (kept beside x).  All of that is exact but for the fp32 sums.  Where x holds an infinity
+// or NaN the bias is subtracted from every code instead, so that they come out as they would.
+//
+// Each group's sum is scaled by its row's scale in fp32; the only rounding to 16 bits is the one of y.  The warps
+// that share a tile's rows split K and meet in shared memory in a fixed order: results do not depend on scheduling.
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "step_ops.cuh"
 
 namespace gbmoe {
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kKBlock = 128;
+constexpr size_t kLinearSmem = 224 * 1024;
 
 struct LinearArgs {
   const void* x;       // [M, K], row stride ldx
@@ -25,24 +43,32 @@ struct LinearArgs {
   const float* scale;  // [N or 2N, K / group]
   void* y;             // [M, N], row stride ldy
   long long ldx, ldy;
-  int M, N, K;
+  int M, N, K, gated, bf16;
+  int wr;              // warps that share a tile's blocks in the row direction (the others split K)
+  // x as the products take it, tokens in tiles of 8, nt tiles (shared memory or workspace)
+  int nt;
+  uint4* xf;           // [blocks][nt][4][32]
+  float* sums;         // [blocks][P + 1][nt * 8]: -8 * 2^-24 * the groups' sums, then 2^(frame + 12)
+  float* odd;          // [blocks][4] not 0 where a block holds infinities or NaN
 };
 
-// Eight int4 codes of one word -> four pairs (k0,k4) (k1,k5) (k2,k6) (k3,k7) of exact floats.
-__device__ __forceinline__ void expand8(__half, uint32_t w, uint32_t r[4]) { s4x8_to_f16x8(w, r); }
-// bf16: a biased nibble (k + 8 in [0, 15]) in the low mantissa bits of 128 (0x4300) reads 128 + (k + 8), since
-// bf16's spacing is 1 on [128, 256); subtracting 136 leaves k exactly.
-__device__ __forceinline__ void expand8(__nv_bfloat16, uint32_t w, uint32_t r[4]) {
-  const __nv_bfloat162 bias = __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308));  // 136
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t v = lop3_sel_xor(w >> (4 * i), 0x000f000fu, 0x43084308u);
-    const __nv_bfloat162 q = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&v), bias);
-    r[i] = *reinterpret_cast<const uint32_t*>(&q);
-  }
+// Pairs (k0,k4) (k1,k5) (k2,k6) (k3,k7) of a word's biased codes: u, 16 u, u, 16 u in units of 2^-24.
+__device__ __forceinline__ void expand8(uint32_t w, uint32_t r[4]) {
+  const uint32_t v = w >> 8;
+  r[0] = lop3_sel_xor(w, 0x000f000fu, 0x00080008u);
+  r[1] = lop3_sel_xor(w, 0x00f000f0u, 0x00800080u);
+  r[2] = lop3_sel_xor(v, 0x000f000fu, 0x00080008u);
+  r[3] = lop3_sel_xor(v, 0x00f000f0u, 0x00800080u);
+}
+// The codes themselves, q or 16 q in units of 2^-24 (exact).
+__device__ __forceinline__ uint32_t unbias2(uint32_t v, uint32_t bias) {
+  const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&bias));
+  return *reinterpret_cast<const uint32_t*>(&q);
 }
 
-template <int G> struct Lanes;  // codes a lane loads of one group: 4 / P words in each of P phases
+template <int RT> constexpr int kInFlight = RT == 1 ? 4 : 2;  // blocks in flight a warp: 128 bytes a lane
+
+template <int G> struct Lanes;  // a lane's codes of a block: 4 / P words in each of P phases (one a group)
 template <> struct Lanes<128> { using Load = uint4; static constexpr int P = 1; };
 template <> struct Lanes<64> { using Load = uint2; static constexpr int P = 2; };
 template <> struct Lanes<32> { using Load = uint32_t; static constexpr int P = 4; };
@@ -52,171 +78,497 @@ template <typename L> __device__ __forceinline__ L load_codes(const uint8_t* p) 
 }
 template <> __device__ __forceinline__ uint4 load_codes<uint4>(const uint8_t* p) { return ld_stream_v4(p); }
 
-template <typename T, int G, int NT, int RT, bool GATED>
-__global__ void __launch_bounds__(kWarps * 32) linear_int4_kernel(LinearArgs a) {
+// One weight block's registers of a warp: codes and scales of RT tiles of 16 rows (rows g and g + 8 a lane).
+template <int G, int RT> struct Block {
+  typename Lanes<G>::Load c[RT][2][Lanes<G>::P];
+  float s[RT][2];  // of group t of the block (t < P), shared in the quad
+};
+
+// One piece: 8 values of x (col, col + 8) of one token, by one of the 16 neighbouring threads of a block and token
+// (c = 0..15, all 16 take part).  Stores the piece, and by one thread each the group's sum and the block's factor.
+template <int G>
+__device__ __forceinline__ bool make_piece(uint4 v, bool bf16, int c, bool live, uint4* xf, float* sums, int ld) {
+  constexpr int P = Lanes<G>::P, WP = 4 / P;
+  const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+  float f[8], top = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 q = bf16 ? Elem<__nv_bfloat16>::unpack(e[j]) : Elem<__half>::unpack(e[j]);
+    f[2 * j] = q.x;
+    f[2 * j + 1] = q.y;
+    top = fmaxf(top, fmaxf(fabsf(q.x), fabsf(q.y)));
+  }
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int fe = x_frame_exp(top);
+  const float mul = exp2i(-fe), low = mul * 0.0625f;
+  // (k0,k4) (k1,k5)/16 (k2,k6) (k3,k7)/16
+  const uint4 h = make_uint4(pack_half2(f[0] * mul, f[4] * mul), pack_half2(f[1] * low, f[5] * low),
+                             pack_half2(f[2] * mul, f[6] * mul), pack_half2(f[3] * low, f[7] * low));
+  const float2 s0 = Elem<__half>::unpack(h.x), s1 = Elem<__half>::unpack(h.y), s2 = Elem<__half>::unpack(h.z), s3 = Elem<__half>::unpack(h.w);
+  float sum = (s0.x + s0.y) + (s2.x + s2.y) + 16.f * ((s1.x + s1.y) + (s3.x + s3.y));
+#pragma unroll
+  for (int o = 1; o < G / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (!live) return false;
+  const int p = c / (G / 8), cp = c % (G / 8), ct = cp / (G / 32), j = p * WP + cp % (G / 32);
+  xf[j * 32 + ct] = h;  // xf: of the block, token tile and token row
+  if (cp == 0) sums[p * ld] = sum * (-8.f * 0x1p-24f);
+  if (c == 0) sums[P * ld] = exp2i(fe + 12);
+  return !(fabsf(sum) < INFINITY);
+}
+
+// The weight stream of a warp: its blocks of every tile of the CTA, in order.
+template <int G, int RT, int NW> struct Stream {
   using LN = Lanes<G>;
-  using Load = typename LN::Load;
-  constexpr int P = LN::P, WP = 4 / P;
-  constexpr int U = RT * NT > 2 ? 2 : 4;  // K blocks in flight a warp
-  __shared__ float red[kWarps][RT * 16][NT * 8 + 1];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t = lane & 3;
-  const int n0 = blockIdx.x * (GATED ? RT * 8 : RT * 16);
-  const int m0 = blockIdx.y * NT * 8;
-  const int kbytes = a.K >> 1, nblk = (a.K + kKBlock - 1) / kKBlock, groups = a.K / G;
-  pdl_trigger();
-  pdl_wait();
+  static constexpr int P = LN::P;
+  const LinearArgs& a;
+  int tile_rows, tiles, wk, wkid, nblk, full, groups, kbytes, rounds, rem, lane_row, wrow_base;
+  int tile, it, blk, round;  // next block
+  bool gated;
+  const uint8_t* wbase;
+  const float* sbase;
+  long long up_w, up_s;
+  uint32_t woff[RT][2], soff[RT][2];
 
-  const uint8_t* wrow[RT][2];
-  const float* srow[RT][2];
-  bool live[RT][2];
+  __device__ __forceinline__ Stream(const LinearArgs& args, int warp, int lane) : a(args) {
+    gated = RT == 2 && a.gated;
+    const int RW = gated ? 16 : RT * 16;
+    wk = NW / a.wr;
+    const int wrow = warp / wk;
+    wkid = warp - wrow * wk;
+    wrow_base = wrow * RW;
+    lane_row = lane >> 2;
+    kbytes = a.K >> 1;
+    nblk = (a.K + kKBlock - 1) / kKBlock;
+    full = a.K / kKBlock;
+    groups = a.K / G;
+    tile_rows = RW * a.wr;
+    tiles = (a.N + tile_rows - 1) / tile_rows;
+    rem = nblk % wk;
+    rounds = ((nblk + wk - 1) / wk + kInFlight<RT> - 1) / kInFlight<RT> * kInFlight<RT>;  // some may be empty
+    up_w = gated ? static_cast<long long>(a.N) * kbytes : 0;
+    up_s = gated ? static_cast<long long>(a.N) * groups : 0;
+    tile = blockIdx.x;
+    it = round = 0;
+    enter(lane & 3);
+  }
+  // first block of the warp in the CTA's it-th tile: the longer shares go round
+  __device__ __forceinline__ int start(int i) const { return (wkid + i * rem) % wk; }
+  __device__ __forceinline__ void enter(int t) {
+    const long long first = min(tile * tile_rows + wrow_base, a.N - 1);
+    wbase = a.w + first * kbytes;
+    sbase = a.scale + first * groups;
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      // GATED: the first half of the row tiles holds gate rows, the second the matching up rows
-      const int local = GATED ? (r % (RT / 2)) * 16 + h * 8 + g : r * 16 + h * 8 + g;
-      const int n = n0 + local;
-      live[r][h] = n < a.N;
-      const long long row = live[r][h] ? (GATED && r >= RT / 2 ? static_cast<long long>(a.N) + n : n) : 0;
-      wrow[r][h] = a.w + row * kbytes;
-      srow[r][h] = a.scale + row * groups;
-    }
-
-  Load buf[U][RT][2][P];
-  float sc[U][RT][2][P];
-  auto fetch = [&](int b, int u) {
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int byte = b * (kKBlock / 2) + p * (G / 2) + t * (G / 8);
-      const int gi = b * P + p;
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const bool ok = live[r][h] && b < nblk && byte < kbytes;
-          buf[u][r][h][p] = ok ? load_codes<Load>(wrow[r][h] + byte) : Load{};
-          sc[u][r][h][p] = live[r][h] && b < nblk && gi < groups ? __ldg(srow[r][h] + gi) : 0.f;
-        }
-    }
-  };
-
-  float acc[RT][NT][4];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.f;
-
-  const T* x = static_cast<const T*>(a.x);
-  auto consume = [&](int b, int u) {
-    if (b >= nblk) return;
-#pragma unroll
-    for (int p = 0; p < P; ++p) {
-      float part[RT][NT][4];
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) part[r][n][i] = 0.f;
-#pragma unroll
-      for (int j = 0; j < WP; ++j) {
-        const int k = b * kKBlock + p * G + t * (G / 4) + 8 * j;
-        uint32_t q[RT][2][4];
+      for (int h = 0; h < 2; ++h) {
+        // rows past the last one read the last one again (and are not written); gated: tile 0 holds gate rows,
+        // tile 1 the matching up rows
+        const uint32_t d = min((gated ? 0 : r * 16) + h * 8 + lane_row, static_cast<int>(a.N - 1 - first));
+        woff[r][h] = d * kbytes + t * (G / 8);
+        soff[r][h] = d * groups + t % P;
+      }
+    blk = start(it);
+  }
+  __device__ __forceinline__ void fetch(Block<G, RT>& d, int t) {
+    if (tile < tiles && blk < nblk) {
+      const uint8_t* wp = wbase + static_cast<long long>(blk) * (kKBlock / 2);
+      const float* sp = sbase + static_cast<long long>(blk) * P;
+      if (blk < full) {
 #pragma unroll
         for (int r = 0; r < RT; ++r)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            expand8(T(), reinterpret_cast<const uint32_t*>(&buf[u][r][h][p])[j], q[r][h]);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const int m = m0 + n * 8 + g;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (m < a.M && k < a.K) v = ld_v4(x + m * a.ldx + k);
-          const uint32_t b0 = __byte_perm(v.x, v.z, 0x5410), b1 = __byte_perm(v.x, v.z, 0x7632);  // (k0,k4) (k1,k5)
-          const uint32_t b2 = __byte_perm(v.y, v.w, 0x5410), b3 = __byte_perm(v.y, v.w, 0x7632);  // (k2,k6) (k3,k7)
+            for (int p = 0; p < P; ++p)
+              d.c[r][h][p] = load_codes<typename LN::Load>(wp + (r == 1 ? up_w : 0) + woff[r][h] + p * (G / 2));
 #pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const uint32_t f0[4] = {q[r][0][0], q[r][1][0], q[r][0][1], q[r][1][1]};
-            mma_16816(T(), part[r][n], f0, b0, b1);
-            const uint32_t f1[4] = {q[r][0][2], q[r][1][2], q[r][0][3], q[r][1][3]};
-            mma_16816(T(), part[r][n], f1, b2, b3);
-          }
-        }
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) d.s[r][h] = __ldg(sp + (r == 1 ? up_s : 0) + soff[r][h]);
+      } else {  // the last block of a K that is no multiple of 128: whole groups are missing
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+              d.c[r][h][p] = blk * P + p < groups ? load_codes<typename LN::Load>(wp + (r == 1 ? up_w : 0) + woff[r][h] + p * (G / 2))
+                                                  : typename LN::Load{};
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            d.s[r][h] = blk * P + t % P < groups ? __ldg(sp + (r == 1 ? up_s : 0) + soff[r][h]) : 0.f;
       }
+    }
+    blk += wk;
+    if (++round == rounds) {
+      round = 0;
+      tile += gridDim.x;
+      ++it;
+      if (tile < tiles) enter(t);
+    }
+  }
+};
+
+// acc += the block's products; xf: the block's pieces (offset of token tile n and step j by `piece`), sums as stored.
+template <int G, int NT, int RT, bool PLAIN, typename Piece>
+__device__ __forceinline__ void multiply(const Block<G, RT>& d, float (&acc)[RT][NT][4], const float* sums, int ld, int t, Piece piece) {
+  constexpr int P = Lanes<G>::P, WP = 4 / P;
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    float part[RT][NT][4];
+    if (p > 0 || !PLAIN) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) part[r][n][i] = 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < WP; ++j) {
+      uint32_t q[RT][2][4];
 #pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int h = 0; h < 2; ++h) {
+          expand8(reinterpret_cast<const uint32_t*>(&d.c[r][h][p])[j], q[r][h]);
+          if constexpr (!PLAIN) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[r][n][i] = fmaf(sc[u][r][i >> 1][p], part[r][n][i], acc[r][n][i]);
+            for (int i = 0; i < 4; ++i) q[r][h][i] = unbias2(q[r][h][i], i & 1 ? 0x00800080u : 0x00080008u);
+          }
+        }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const uint4 v = piece(n, p * WP + j);
+        if (PLAIN && j == 0) {
+          const float2 c = *reinterpret_cast<const float2*>(sums + p * ld + n * 8 + 2 * t);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) { part[r][n][0] = part[r][n][2] = c.x; part[r][n][1] = part[r][n][3] = c.y; }
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const uint32_t f0[4] = {q[r][0][0], q[r][1][0], q[r][0][1], q[r][1][1]};
+          mma_f16_16816(part[r][n], f0, v.x, v.y);
+          const uint32_t f1[4] = {q[r][0][2], q[r][1][2], q[r][0][3], q[r][1][3]};
+          mma_f16_16816(part[r][n], f1, v.z, v.w);
+        }
+      }
+    }
+    float sc[RT][2];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) sc[r][h] = P == 1 ? d.s[r][h] : __shfl_sync(0xffffffffu, d.s[r][h], (threadIdx.x & 28) | p);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float2 fac = *reinterpret_cast<const float2*>(sums + P * ld + n * 8 + 2 * t);
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[r][n][i] = fmaf(sc[r][i >> 1], part[r][n][i] * (i & 1 ? fac.y : fac.x), acc[r][n][i]);
+    }
+  }
+}
+
+// The warps of a row group meet ([warp][token][row] in shared memory) and y is written.
+template <int NT, int RT, int NW>
+__device__ __forceinline__ void join_and_write(const LinearArgs& a, const float (&acc)[RT][NT][4], float* red, int tile, int wk,
+                                               bool gated, int m0, int live_m) {
+  constexpr int PR = RT * 16 + 4;  // row pitch: no bank conflicts
+  constexpr int NC = NT < 4 ? NT : 4;  // token tiles at once: room in shared memory
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int RW = gated ? 16 : RT * 16, wr = NW / wk;
+  float* mine = red + warp * (NC * 8 * PR);
+#pragma unroll
+  for (int c = 0; c < NT; c += NC) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          mine[(n * 8 + 2 * t + (i & 1)) * PR + r * 16 + (i >> 1) * 8 + g] = acc[r][c + n][i];
+    __syncthreads();
+    for (int i = tid; i < wr * NC * 8 * RW; i += NW * 32) {  // [row group][token][row], powers of two
+      const int r = i & (RW - 1), gm = i / RW, m = gm % (NC * 8), grp = gm / (NC * 8);
+      const int n = (tile * wr + grp) * RW + r;
+      if (n >= a.N || c * 8 + m >= live_m) continue;
+      const float* src = red + grp * wk * (NC * 8 * PR) + m * PR + r;
+      float v = 0.f;
+      for (int w = 0; w < wk; ++w) v += src[w * (NC * 8 * PR)];
+      v *= 4096.f;
+      if (gated) {
+        float up = 0.f;
+        for (int w = 0; w < wk; ++w) up += src[w * (NC * 8 * PR) + 16];
+        v = silu_f32(v) * (up * 4096.f);
+      }
+      const long long at = (m0 + c * 8 + m) * a.ldy + n;
+      if (a.bf16) static_cast<__nv_bfloat16*>(a.y)[at] = __float2bfloat16_rn(v);
+      else static_cast<__half*>(a.y)[at] = __float2half_rn(v);
+    }
+    __syncthreads();
+  }
+}
+
+// Up to 8 tokens, x in shared memory.
+template <int G, int RT, int NW>
+__global__ void __launch_bounds__(NW * 32, 1) linear_int4_kernel(LinearArgs a) {
+  constexpr int P = Lanes<G>::P, U = kInFlight<RT>;
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ int odd;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = lane & 3;
+  float* red = reinterpret_cast<float*>(smem);
+  uint4* xf = reinterpret_cast<uint4*>(smem + NW * 8 * (RT * 16 + 4) * 4);
+  const int nblk = (a.K + kKBlock - 1) / kKBlock;
+  float* sums = reinterpret_cast<float*>(xf + nblk * 128);
+  pdl_trigger();
+  if (tid == 0) odd = 0;
+  pdl_wait();
+  Stream<G, RT, NW> st(a, warp, lane);
+  Block<G, RT> buf[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) st.fetch(buf[u], t);
+  __syncthreads();
+
+  // tokens past the last one are left as they are: columns of a product do not mix
+  constexpr int B = 7;  // loads in flight a thread
+  const int pieces = nblk * a.M * 16;
+  for (int w0 = warp * 32; w0 < pieces; w0 += B * NW * 32) {  // whole warps: the threads of a piece talk to each other
+    uint4 v[B];
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const int i = w0 + lane + k * NW * 32, bm = i >> 4, b = bm / a.M, m = bm - b * a.M, col = b * kKBlock + (i & 15) * 8;
+      v[k] = make_uint4(0, 0, 0, 0);
+      if (i < pieces && col < a.K) v[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ldx + col);
+    }
+#pragma unroll
+    for (int k = 0; k < B; ++k) {
+      const int i = w0 + lane + k * NW * 32, bm = i >> 4, b = bm / a.M, m = bm - b * a.M;
+      if (w0 + k * NW * 32 >= pieces) break;
+      if (make_piece<G>(v[k], a.bf16, i & 15, i < pieces, xf + b * 128 + m * 4, sums + b * (P + 1) * 8 + m, 8)) odd = 1;
+    }
+  }
+  __syncthreads();
+  const bool plain = !odd;
+  for (int it = 0, tile = blockIdx.x; tile < st.tiles; ++it, tile += gridDim.x) {
+    float acc[RT][1][4];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[r][0][i] = 0.f;
+    int blk = st.start(it);
+    auto run = [&](auto p) {
+      for (int rd = 0; rd < st.rounds; rd += U)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (blk < nblk)
+            multiply<G, 1, RT, decltype(p)::value>(buf[u], acc, sums + blk * (P + 1) * 8, 8, t,
+                                                   [&](int, int j) { return xf[blk * 128 + j * 32 + lane]; });
+          blk += st.wk;
+          st.fetch(buf[u], t);
+        }
+    };
+    if (plain) run(std::true_type{}); else run(std::false_type{});
+    join_and_write<1, RT, NW>(a, acc, red, tile, st.wk, st.gated, 0, a.M);
+  }
+}
+
+// x into the workspace: one CTA a block of K, 16 threads a token.
+template <int G>
+__global__ void __launch_bounds__(256) linear_pieces_kernel(LinearArgs a) {
+  constexpr int P = Lanes<G>::P;
+  pdl_trigger();
+  pdl_wait();
+  const int b = blockIdx.x, c = threadIdx.x & 15, col = b * kKBlock + c * 8;
+  bool odd = false;
+  for (int m0 = 0; m0 < a.M; m0 += 16) {
+    const int m = m0 + (threadIdx.x >> 4);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (m < a.M && col < a.K) v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ldx + col);
+    odd |= make_piece<G>(v, a.bf16, c, m < a.M, a.xf + (static_cast<long long>(b) * a.nt + (m >> 3)) * 128 + (m & 7) * 4,
+                         a.sums + static_cast<long long>(b) * (P + 1) * a.nt * 8 + m, a.nt * 8);
+  }
+  odd = __syncthreads_or(odd);
+  if (threadIdx.x < 4) a.odd[b * 4 + threadIdx.x] = odd ? 1.f : 0.f;
+}
+
+// Any M and K, x from the workspace: NT tiles of 8 tokens a CTA, a ring of R steps (quarters of a block) a warp.
+template <int G, int NT, int NW> struct WideCfg {
+  static constexpr int R = NT == 8 ? 4 : 8;
+  static constexpr int kSums = (Lanes<G>::P + 1) * NT * 32 + 16;        // bytes of a block's sums, factors and mark
+  static constexpr int kWarp = R * NT * 512 + 4 * kSums;                // ring, then the sums of four blocks
+  static constexpr size_t kSmem = static_cast<size_t>(NW) * (kWarp + (NT < 4 ? NT : 4) * 8 * 36 * 4);
+  static_assert(kSmem <= kLinearSmem, "shared memory");
+};
+
+template <int G, int NT, int NW>
+__global__ void __launch_bounds__(NW * 32, 1) linear_int4_wide_kernel(LinearArgs a) {
+  using W = WideCfg<G, NT, NW>;
+  constexpr int P = Lanes<G>::P, RT = 2, U = kInFlight<RT>, R = W::R;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = lane & 3;
+  unsigned char* ring = smem + warp * W::kWarp;
+  float* red = reinterpret_cast<float*>(smem + NW * W::kWarp);
+  const int nt0 = blockIdx.y * NT, m0 = nt0 * 8, live_m = min(NT * 8, a.M - m0);
+  pdl_trigger();
+  pdl_wait();
+  Stream<G, RT, NW> st(a, warp, lane);
+  Block<G, RT> buf[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) st.fetch(buf[u], t);
+
+  // the stream of x: the steps of the same blocks, R steps ahead; token tiles past the last one repeat it
+  int x_tile = blockIdx.x, x_it = 0, x_blk = st.start(0), x_round = 0, x_sums = 0;
+  auto issue = [&](int j, int slot) {  // step j of the next block
+    if (x_tile < st.tiles && x_blk < st.nblk) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const long long at = (static_cast<long long>(x_blk) * a.nt + min(nt0 + n, a.nt - 1)) * 4 + j;
+        cp_async16_ca(ring + (slot * NT + n) * 512 + lane * 16, a.xf + at * 32 + lane);
+      }
+      if (j == 0)
+        for (int i = lane; i <= (P + 1) * NT * 2; i += 32) {
+          const int p = i / (NT * 2), q = i % (NT * 2), tl = min(nt0 + (q >> 1), a.nt - 1);
+          const float* src = p > P ? a.odd + x_blk * 4
+                                   : a.sums + (static_cast<long long>(x_blk) * (P + 1) + p) * a.nt * 8 + tl * 8 + (q & 1) * 4;
+          cp_async16_ca(ring + R * NT * 512 + x_sums * W::kSums + i * 16, src);
+        }
+    }
+    cp_commit();
+    if (j == 3) {
+      x_sums = (x_sums + 1) & 3;
+      x_blk += st.wk;
+      if (++x_round == st.rounds) { x_round = 0; x_tile += gridDim.x; x_blk = st.start(++x_it); }
     }
   };
-
 #pragma unroll
-  for (int u = 0; u < U; ++u) fetch(warp + u * kWarps, u);
-  for (int b = warp; b < nblk; b += U * kWarps) {
+  for (int i = 0; i < R; ++i) issue(i & 3, i);
+  int c_sums = 0;
+  for (int it = 0, tile = blockIdx.x; tile < st.tiles; ++it, tile += gridDim.x) {
+    float acc[RT][NT][4];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      consume(b + u * kWarps, u);
-      fetch(b + (U + u) * kWarps, u);
-    }
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.f;
+    int blk = st.start(it);
+    for (int rd = 0; rd < st.rounds; rd += U)
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int s0 = R == 8 ? u * 4 : 0;  // the block's first slot
+        if (blk < st.nblk) {
+          const float* sums = reinterpret_cast<const float*>(ring + R * NT * 512 + c_sums * W::kSums);
+          cp_wait<R - 1>();  // the block's first step, its sums and mark
+          __syncwarp();      // which other lanes fetched; the pieces of a lane are its own
+          auto piece = [&](int n, int j) {
+            if (n == 0 && j > 0) cp_wait<R - 1>();
+            const uint4 v = *reinterpret_cast<const uint4*>(ring + ((s0 + j) * NT + n) * 512 + lane * 16);
+            if (n == NT - 1) issue(j, s0 + j);
+            return v;
+          };
+          if (sums[(P + 1) * NT * 8] == 0.f) multiply<G, NT, RT, true>(buf[u], acc, sums, NT * 8, t, piece);
+          else multiply<G, NT, RT, false>(buf[u], acc, sums, NT * 8, t, piece);
+          __syncwarp();      // all have read the sums
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) issue(j, s0 + j);
+        }
+        c_sums = (c_sums + 1) & 3;
+        blk += st.wk;
+        st.fetch(buf[u], t);
+      }
+    join_and_write<NT, RT, NW>(a, acc, red, tile, st.wk, st.gated, m0, live_m);
   }
+  cp_wait<0>();
+}
 
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) red[warp][r * 16 + (i >> 1) * 8 + g][n * 8 + 2 * t + (i & 1)] = acc[r][n][i];
-  __syncthreads();
-  constexpr int ROWS = GATED ? RT * 8 : RT * 16;
-  T* y = static_cast<T*>(a.y);
-  for (int i = threadIdx.x; i < ROWS * NT * 8; i += kWarps * 32) {
-    const int r = i % ROWS, m = i / ROWS;
-    if (n0 + r >= a.N || m0 + m >= a.M) continue;
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += red[w][r][m];
-    if constexpr (GATED) {
-      float up = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) up += red[w][ROWS + r][m];
-      v = silu_f32(v) * up;
-    }
-    y[(m0 + m) * a.ldy + n0 + r] = Elem<T>::from_float(v);
+// Blocks of K that a CTA of the one-launch kernel can hold.
+template <int G> constexpr int kResidentBlocks = static_cast<int>((kLinearSmem - 16 * 8 * 36 * 4) / (2048 + (Lanes<G>::P + 1) * 32));
+
+// Warps that share a tile's blocks: the split of least time, counted in blocks a warp (a tile's join costs one).
+int choose_wr(const LinearArgs& a, int RW, int NW, int sms) {
+  const int nblk = (a.K + kKBlock - 1) / kKBlock;
+  long long best = -1;
+  int wr = 1;
+  for (int r = 1; r <= NW; r *= 2) {
+    const long long tiles = (a.N + static_cast<long long>(RW) * r - 1) / (static_cast<long long>(RW) * r), wk = NW / r;
+    const long long cost = (tiles + sms - 1) / sms * ((nblk + wk - 1) / wk + 1);
+    if (best < 0 || cost < best) { best = cost; wr = r; }
   }
+  return wr;
 }
 
-template <typename T, int G, int NT, int RT, bool GATED>
-cudaError_t launch_one(const LinearArgs& a, cudaStream_t s) {
-  const int rows = GATED ? RT * 8 : RT * 16;
-  const dim3 grid((a.N + rows - 1) / rows, (a.M + NT * 8 - 1) / (NT * 8));
-  return launch_kernel(linear_int4_kernel<T, G, NT, RT, GATED>, grid, dim3(kWarps * 32), 0, s, true, a);
+template <int G, int RT>
+cudaError_t launch_resident(LinearArgs a, int sms, cudaStream_t s) {
+  constexpr int NW = 16;
+  const int RW = a.gated ? 16 : RT * 16, nblk = (a.K + kKBlock - 1) / kKBlock;
+  a.wr = choose_wr(a, RW, NW, sms);
+  const int tiles = (a.N + RW * a.wr - 1) / (RW * a.wr);
+  auto kern = linear_int4_kernel<G, RT, NW>;
+  cudaError_t err = set_smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(kLinearSmem));
+  if (err != cudaSuccess) return err;
+  const size_t smem = NW * 8 * (RT * 16 + 4) * 4 + static_cast<size_t>(nblk) * (2048 + (Lanes<G>::P + 1) * 32);
+  return launch_kernel(kern, dim3(tiles < sms ? tiles : sms), dim3(NW * 32), smem, s, true, a);
 }
 
-template <typename T, int G>
-cudaError_t launch_linear(const LinearArgs& a, bool gated, cudaStream_t s) {
-  if (a.M <= 8) return gated ? launch_one<T, G, 1, 2, true>(a, s) : launch_one<T, G, 1, 1, false>(a, s);
-  if (a.M <= 16) return gated ? launch_one<T, G, 2, 2, true>(a, s) : launch_one<T, G, 2, 2, false>(a, s);
-  return gated ? launch_one<T, G, 4, 2, true>(a, s) : launch_one<T, G, 4, 2, false>(a, s);
+template <int G, int NT, int NW>
+cudaError_t launch_wide(LinearArgs a, int sms, cudaStream_t s) {
+  const int RW = a.gated ? 16 : 32, nblk = (a.K + kKBlock - 1) / kKBlock;
+  cudaError_t err = launch_kernel(linear_pieces_kernel<G>, dim3(nblk), dim3(256), 0, s, true, a);
+  if (err != cudaSuccess) return err;
+  a.wr = choose_wr(a, RW, NW, sms);
+  const int tiles = (a.N + RW * a.wr - 1) / (RW * a.wr);
+  auto kern = linear_int4_wide_kernel<G, NT, NW>;
+  constexpr int smem = static_cast<int>(WideCfg<G, NT, NW>::kSmem);
+  err = set_smem_limit_once(reinterpret_cast<const void*>(kern), smem);
+  if (err != cudaSuccess) return err;
+  return launch_kernel(kern, dim3(tiles < sms ? tiles : sms, (a.nt + NT - 1) / NT), dim3(NW * 32), smem, s, true, a);
 }
 
-template <typename T>
-cudaError_t launch_typed(const LinearArgs& a, int group, bool gated, cudaStream_t s) {
-  if (group == 128) return launch_linear<T, 128>(a, gated, s);
-  if (group == 64) return launch_linear<T, 64>(a, gated, s);
-  return launch_linear<T, 32>(a, gated, s);
+template <int G>
+cudaError_t launch_linear(const LinearArgs& a, int sms, cudaStream_t s) {
+  if (!a.xf) {
+    // 16 or 32 rows a warp: whichever leaves the busiest SM with fewer rows
+    const int t1 = (a.N + 15) / 16, t2 = (a.N + 31) / 32;
+    const int r1 = (t1 + sms - 1) / sms * 16, r2 = (t2 + sms - 1) / sms * 32;
+    return !a.gated && r1 < r2 ? launch_resident<G, 1>(a, sms, s) : launch_resident<G, 2>(a, sms, s);
+  }
+  if (a.nt == 1) return launch_wide<G, 1, 16>(a, sms, s);
+  if (a.nt == 2) return launch_wide<G, 2, 16>(a, sms, s);
+  if (a.nt <= 4) return launch_wide<G, 4, 8>(a, sms, s);
+  return launch_wide<G, 8, 8>(a, sms, s);
+}
+
+struct LinearLayout { size_t sums = 0, odd = 0, total = 0; };  // the pieces stand first
+bool linear_layout(int M, int K, int group, LinearLayout* l) {  // false: no workspace is needed
+  const int nblk = (K + kKBlock - 1) / kKBlock;
+  const int fit = group == 128 ? kResidentBlocks<128> : group == 64 ? kResidentBlocks<64> : kResidentBlocks<32>;
+  if (M <= 8 && nblk <= fit) return false;
+  const size_t nt = (static_cast<size_t>(M) + 7) / 8;
+  l->sums = nblk * nt * 2048;
+  l->odd = l->sums + nblk * nt * 32 * (128 / group + 1);
+  l->total = l->odd + static_cast<size_t>(nblk) * 16;
+  return true;
 }
 
 }  // namespace
 }  // namespace gbmoe
 
+extern "C" size_t moe_linear_int4_workspace_size(int M, int K, int group) {
+  using namespace gbmoe;
+  LinearLayout l;
+  if (M <= 0 || M > (1 << 20) || K <= 0 || K > (1 << 25) || (group != 32 && group != 64 && group != 128) || K % group) return 0;
+  return linear_layout(M, K, group, &l) ? l.total : 0;
+}
+
 extern "C" moe_status_t moe_linear_int4(int dtype, const void* x, int64_t x_stride, const uint8_t* w, const float* w_scale,
                                         int M, int N, int K, int group, int gated, void* y, int64_t y_stride,
-                                        moe_stream_t stream) {
+                                        void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   using namespace gbmoe;
   return guarded("moe_linear_int4", [&]() -> moe_status_t {
     auto bad = [](const char* m) { return report_error(MOE_ERR_INVALID_ARG, std::string("moe_linear_int4: ") + m); };
@@ -226,16 +578,27 @@ extern "C" moe_status_t moe_linear_int4(int dtype, const void* x, int64_t x_stri
       return report_error(MOE_ERR_UNSUPPORTED, "moe_linear_int4: the group size must be 32, 64 or 128");
     if (K % group) return bad("K must be a multiple of the group size");
     if (gated != 0 && gated != 1) return bad("gated must be 0 or 1");
-    if (M > (1 << 20) || N > (1 << 29) || K > (1 << 30))
+    if (M > (1 << 20) || N > (1 << 29) || K > (1 << 25))
       return report_error(MOE_ERR_UNSUPPORTED, "moe_linear_int4: problem too large");
     if (M == 0) return MOE_OK;
     if (!x || !w || !w_scale || !y) return bad("NULL pointer");
     if (x_stride < K || y_stride < N) return bad("rows overlap: a row stride is shorter than its row");
     if (!aligned(x, 16) || x_stride % 8 || !aligned(w, 16)) return bad("x rows and w must start on 16 bytes");
     if (!aligned(w_scale, 4) || !aligned(y, 2)) return bad("unaligned scales or output");
-    const LinearArgs a{x, w, w_scale, y, x_stride, y_stride, M, N, K};
+    const int sms = num_sms_current();
+    if (sms <= 0) return report_error(MOE_ERR_CUDA, "moe_linear_int4: no CUDA device");
+    LinearArgs a{x, w, w_scale, y, x_stride, y_stride, M, N, K, gated, dtype == MOE_DTYPE_BF16, 1, (M + 7) / 8, nullptr, nullptr, nullptr};
+    LinearLayout l;
+    if (linear_layout(M, K, group, &l)) {
+      if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256))
+        return report_error(MOE_ERR_WORKSPACE, "moe_linear_int4: workspace NULL, misaligned or too small");
+      char* ws = static_cast<char*>(workspace);
+      a.xf = reinterpret_cast<uint4*>(ws);
+      a.sums = reinterpret_cast<float*>(ws + l.sums);
+      a.odd = reinterpret_cast<float*>(ws + l.odd);
+    }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return launched("moe_linear_int4", dtype == MOE_DTYPE_FP16 ? launch_typed<__half>(a, group, gated, s)
-                                                               : launch_typed<__nv_bfloat16>(a, group, gated, s));
+    return launched("moe_linear_int4", group == 128 ? launch_linear<128>(a, sms, s)
+                                       : group == 64 ? launch_linear<64>(a, sms, s) : launch_linear<32>(a, sms, s));
   });
 }

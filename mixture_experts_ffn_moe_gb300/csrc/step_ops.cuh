@@ -48,6 +48,17 @@ __device__ __forceinline__ void mma_16816(__nv_bfloat16, float d[4], const uint3
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Asynchronous 16-byte copies to shared memory: through L2 only, zeros where !ok; or through L1.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async16_ca(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))), "l"(src)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // Division of 0 <= n < 2^31 by a fixed 1 <= d < 2^31: q = (n * mul) >> (32 + shift) with
 // mul = ceil(2^(32 + shift) / d) and shift = ceil(log2 d) - 1, which is exact on that range
 // (Granlund and Montgomery 1994, "Division by invariant integers using multiplication").

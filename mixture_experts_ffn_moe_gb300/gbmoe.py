@@ -77,7 +77,8 @@ _SIGS = {
     "moe_profile_enable": (_i, [_i]),
     "moe_profile_read": (_i, [_vp, _vp, _i, _vp, _vp]),
     "moe_rope": (_i, [_vp, _vp]),
-    "moe_linear_int4": (_i, [_i, _vp, _i64, _vp, _vp] + [_i] * 5 + [_vp, _i64, _vp]),
+    "moe_linear_int4_workspace_size": (_sz, [_i] * 3),
+    "moe_linear_int4": (_i, [_i, _vp, _i64, _vp, _vp] + [_i] * 5 + [_vp, _i64, _vp, _sz, _vp]),
     "moe_tree_attention_workspace_size": (_sz, [_i] * 5),
     "moe_tree_attention": (_i, [_vp, _vp, _sz, _vp]),
     "moe_read_tree_status": (_i, [_vp, _vp, _vp]),
@@ -598,7 +599,11 @@ def moe_rope_append(q, k, v, positions, inv_freq, slots, k_cache, v_cache, scale
     return q_out
 
 
-def moe_linear_int4(x, w, w_scale, gated=False, out=None):
+def moe_linear_int4_workspace_size(M, K, group) -> int:
+    return int(load().moe_linear_int4_workspace_size(M, K, group))
+
+
+def moe_linear_int4(x, w, w_scale, gated=False, out=None, workspace=None):
     """x [M, K] (bf16 / fp16) times 4-bit weights w uint8 [N, K/2] with w_scale fp32 [N, K/group]: [M, N].
 
     gated: w holds 2N rows, gate rows first; SiLU(gate) * up of shape [M, N].  See include/gbmoe.h.
@@ -618,9 +623,16 @@ def moe_linear_int4(x, w, w_scale, gated=False, out=None):
         out = torch.empty((M, N), dtype=x.dtype, device=x.device)
     elif out.dtype != x.dtype or not out.is_cuda or tuple(out.shape) != (M, N) or (N > 1 and out.stride(1) != 1):
         raise ValueError("out must be [M, N] of x's type with contiguous rows")
-    st = load().moe_linear_int4(dt, x.data_ptr(), x.stride(0) if M > 1 else K, w.data_ptr(), w_scale.data_ptr(), M, N,
-                                K, K // groups, 1 if gated else 0, out.data_ptr(), out.stride(0) if M > 1 else N,
-                                _raw_stream(x))
+    lib, group, ws, ws_bytes = load(), K // groups, 0, 0
+    if workspace is None and (M > 8 or K > 8192):
+        n = lib.moe_linear_int4_workspace_size(M, K, group)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel()
+    st = lib.moe_linear_int4(dt, x.data_ptr(), x.stride(0) if M > 1 else K, w.data_ptr(), w_scale.data_ptr(), M, N, K,
+                             group, 1 if gated else 0, out.data_ptr(), out.stride(0) if M > 1 else N, ws, ws_bytes,
+                             _raw_stream(x))
     if st:
         _check(st, "moe_linear_int4")
     return out

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from _step_ops import ancestors, linear_ref, mask_tensor, rope_ref, tree_ref, verify_ref
+from _step_ops import ancestors, int4_values, linear_ref, mask_tensor, rope_ref, tree_ref, verify_ref
 from mixture_experts_ffn_moe_gb300 import build, gbmoe
 
 pytestmark = pytest.mark.gpu
@@ -158,6 +158,25 @@ def test_linear_int4_every_code_and_wide_ranges():
     s = torch.exp2(torch.randint(-30, 21, (N, 2), generator=g).float())
     x = (torch.randn(4, K, generator=g) * torch.tensor([1e-30, 1.0, 1e4, 1e25])[:, None]).to(BF)
     close(gbmoe.moe_linear_int4(x.cuda(), w.cuda(), s.cuda()), *linear_ref(x, w, s, False))
+
+
+@pytest.mark.parametrize("dt,M,K", [(BF, 3, 512), (FP, 12, 512), (BF, 40, 8192)])
+def test_linear_int4_infinities_and_sums_near_overflow(dt, M, K):
+    """An infinite activation gives infinities of the code's sign; sums of x past the type's range do no harm."""
+    g = gen(6)
+    N, K = 40, K
+    x = torch.randn(M, K, generator=g).to(dt)
+    x[0] = torch.finfo(dt).max / 64 if dt == FP else 1e35
+    x[1, 7] = float("inf")
+    w = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
+    w[:, 3] = torch.where((w[:, 3] >> 4) == 0, w[:, 3] + 16, w[:, 3])  # column 7 has no zero codes
+    s = (0.5 + torch.rand(N, K // 128, generator=g)) * 1e-3
+    y = gbmoe.moe_linear_int4(x.cuda(), w.cuda(), s.cuda())
+    ref, bound = linear_ref(x, w, s, False)
+    keep = [m for m in range(M) if m != 1]
+    close(y[keep], ref[keep], bound[keep])
+    q7 = int4_values(w)[:, 7]
+    assert (y[1].float().cpu() == torch.where(q7 > 0, float("inf"), float("-inf"))).all()
 
 
 def test_linear_int4_strided_rows_and_nonfinite_rows_stay_apart():

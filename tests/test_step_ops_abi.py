@@ -53,8 +53,8 @@ def test_rope_refusals(lib):
     assert b"moe_rope" in lib.moe_last_error()
 
 
-def linear(lib, dtype=0, x=P, xs=256, w=P, s=P, M=4, N=64, K=256, group=128, gated=0, y=P, ys=64):
-    return lib.moe_linear_int4(dtype, x, xs, w, s, M, N, K, group, gated, y, ys, None)
+def linear(lib, dtype=0, x=P, xs=256, w=P, s=P, M=4, N=64, K=256, group=128, gated=0, y=P, ys=64, ws=None, size=0):
+    return lib.moe_linear_int4(dtype, x, xs, w, s, M, N, K, group, gated, y, ys, ws, size, None)
 
 
 def test_linear_refusals(lib):
@@ -73,6 +73,9 @@ def test_linear_refusals(lib):
     assert linear(lib, xs=260) == 1
     assert linear(lib, w=P + 4) == 1
     assert linear(lib, y=P + 1) == 1
+    need = gbmoe.moe_linear_int4_workspace_size(16, 256, 128)
+    assert need > 0 and gbmoe.moe_linear_int4_workspace_size(8, 256, 128) == 0
+    assert gbmoe.moe_linear_int4_workspace_size(1, 1 << 16, 32) > 0 and gbmoe.moe_linear_int4_workspace_size(16, 200, 128) == 0
 
 
 TREE = dict(dtype=0, nodes=8, batch=2, hq=4, hk=2, dim=128, page=16, pages=10, width=4, scale=0.1, tld=4, q=P, k=P, v=P,
