@@ -19,111 +19,16 @@
 // warps never wait for each other inside a unit.
 #include <cuda_runtime.h>
 
-#include "sm100_ptx.cuh"
-#include "step_ops.cuh"
+#include "tree_attention.cuh"
 
 namespace gbmoe {
 namespace {
 
+using namespace tree;
+
 constexpr int kAWarps = 4;
 constexpr int kAThreads = kAWarps * 32;
 constexpr int kTile = kAWarps * 16;  // cache slots a tile
-constexpr int kMaxBatch = 1024;
-constexpr int kMaxTreeCtas = 320;    // CTAs that the workspace has room for
-constexpr float kLazy = 8.f;         // growth of a row's maximum (in powers of two) that moves its reference
-
-struct TreeArgs {
-  const void* q;
-  const void* kc;
-  const void* vc;
-  void* out;
-  const int32_t* table;
-  const int32_t* ctx;
-  const int32_t* offs;
-  const unsigned long long* mask;  // null: a chain
-  long long q_t, q_h, o_t, o_h;
-  long long k_page, k_slot, k_head, v_page, v_slot, v_head;
-  long long table_ld;
-  int N, B, Hq, Hkv, pages, table_w;
-  FastDiv page, group;
-  float scale_log2;
-  int32_t* header;    // workspace: [0] CTAs, [1] bad lengths, offsets or counts, then bad pages of every CTA
-  long long* prefix;  // [B + 1] first tile of every sequence, [B + 1] = tiles a CTA
-  float* part_o;      // [CTAs * 2][rows][D]
-  float* part_ml;     // [CTAs * 2][rows][2]
-};
-
-__device__ __forceinline__ void ldm4(uint32_t a, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
-}
-__device__ __forceinline__ void ldm4t(uint32_t a, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-// Words of two 16-bit elements: does either hold an infinity or NaN?
-__device__ __forceinline__ bool nonfinite2(__nv_bfloat16, uint32_t w) {
-  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
-}
-__device__ __forceinline__ bool nonfinite2(__half, uint32_t w) {
-  return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
-}
-
-// Committed slots and nodes of sequence b, brought into range (bad counts what had to be).
-__device__ __forceinline__ void seq_sizes(const TreeArgs& a, int b, int& ctx, int& n, int& bad) {
-  const int lo = a.offs[b], hi = a.offs[b + 1];
-  ctx = a.ctx[b];
-  n = hi - lo;
-  bad = 0;
-  const long long room = static_cast<long long>(a.table_w) * a.page.d;
-  if (lo < 0 || hi < lo || hi > a.N || n > MOE_MAX_TREE_NODES || n > room) { n = 0; bad = 1; }
-  if (ctx < 0) { ctx = 0; bad = 1; }
-  if (ctx > room - n) { ctx = static_cast<int>(room - n); bad = 1; }
-}
-
-// prefix[b] = first tile of sequence b on the line of all tiles; rows = rows of a unit's row tile.
-__device__ __forceinline__ void plan_line(const TreeArgs& a, int rows, long long* prefix, long long* scratch, int* bad) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long base = 0;
-  int nbad = 0;
-  for (int b0 = 0; b0 < a.B; b0 += kAThreads) {
-    const int b = b0 + tid;
-    long long tiles = 0;
-    if (b < a.B) {
-      int ctx, n, bd;
-      seq_sizes(a, b, ctx, n, bd);
-      nbad += bd;
-      if (n > 0) {
-        const int rt = (n * static_cast<int>(a.group.d) + rows - 1) / rows;
-        tiles = static_cast<long long>(a.Hkv) * rt * ((static_cast<long long>(ctx) + n + kTile - 1) / kTile);
-      }
-    }
-    long long incl = tiles;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
-    }
-    if (lane == 31) scratch[warp] = incl;
-    __syncthreads();
-    long long before = base, all = 0;
-    for (int w = 0; w < kAWarps; ++w) {
-      if (w < warp) before += scratch[w];
-      all += scratch[w];
-    }
-    if (b < a.B) prefix[b] = before + incl - tiles;
-    base += all;
-    __syncthreads();
-  }
-  if (tid == 0) prefix[a.B] = base;
-  *bad = nbad;
-  __syncthreads();
-}
 
 template <int D> struct TreeCfg {
   static constexpr int kRow = D * 2;                     // bytes of a cache row
@@ -154,7 +59,7 @@ __global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
   pdl_trigger();
   pdl_wait();
   int bad_plan;
-  plan_line(a, R, prefix, prefix + a.B + 1, &bad_plan);
+  plan_line<kAThreads>(a, prefix, prefix + a.B + 1, &bad_plan);
   const long long total = prefix[a.B];
   const long long chunk = (total + gridDim.x - 1) / gridDim.x;
   if (blockIdx.x == 0) {
@@ -166,24 +71,9 @@ __global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
   long long pos = blockIdx.x * chunk;
   const long long end = pos + chunk < total ? pos + chunk : total;
   while (pos < end) {
-    int b;
-    {
-      int lo = 0, hi = a.B;  // prefix[lo] <= pos < prefix[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= pos) lo = mid; else hi = mid;
-      }
-      b = lo;
-    }
-    int ctx, n, bd;
-    seq_sizes(a, b, ctx, n, bd);
-    const int L = ctx + n, kt = (L + kTile - 1) / kTile;
-    const int rt_n = (n * static_cast<int>(a.group.d) + R - 1) / R;
-    const long long rel = pos - prefix[b];
-    const int unit = static_cast<int>(rel / kt), k0 = static_cast<int>(rel - static_cast<long long>(unit) * kt);
-    const int k1 = static_cast<int>(end - pos < kt - k0 ? k0 + (end - pos) : kt);
-    const int head = unit / rt_n, row0 = (unit - head * rt_n) * R;
-    const int rows = min(R, n * static_cast<int>(a.group.d) - row0), node0 = a.offs[b];
+    const Piece u = piece_at(a, prefix, pos, end, 0);
+    const int b = u.b, ctx = u.ctx, L = u.ctx + u.n, kt = u.kt, k0 = u.k0, k1 = u.k1, head = u.head, row0 = u.row0;
+    const int rows = u.rows, node0 = u.node0;
     const T* kbase = static_cast<const T*>(a.kc) + head * a.k_head;
     const T* vbase = static_cast<const T*>(a.vc) + head * a.v_head;
     const int32_t* table = a.table + b * a.table_ld;
@@ -438,7 +328,7 @@ __global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
 }
 
 // Joins the parts of units that were cut; one warp a row (node, query head).
-template <typename T, int D, int R>
+template <typename T, int D>
 __global__ void __launch_bounds__(128) tree_join_kernel(TreeArgs a) {
   pdl_trigger();
   pdl_wait();
@@ -458,15 +348,15 @@ __global__ void __launch_bounds__(128) tree_join_kernel(TreeArgs a) {
   const int j = i - a.offs[b];
   if (j < 0 || j >= n) return;
   const int group = a.group.d, head = hq / group, r = j * group + (hq - head * group);
-  const int kt = (ctx + n + kTile - 1) / kTile, rt_n = (n * group + R - 1) / R;
+  const int kt = (ctx + n + a.tile - 1) / a.tile, per = a.rows * a.ranks, rt_n = (n * group + per - 1) / per;
   const long long chunk = a.prefix[a.B + 1];
-  const long long s = a.prefix[b] + (static_cast<long long>(head) * rt_n + r / R) * kt, e = s + kt;
+  const long long s = a.prefix[b] + (static_cast<long long>(head) * rt_n + r / per) * kt, e = s + kt;
   const long long c0 = s / chunk, c1 = (e - 1) / chunk;
   if (c0 == c1) return;
-  const int row = r % R, parts = static_cast<int>(c1 - c0 + 1);
+  const int rank = r % per / a.rows, row = r % a.rows, parts = static_cast<int>(c1 - c0 + 1);
   auto at = [&](int p) {
     const long long c = c0 + p;
-    return (c * 2 + (c * chunk > s ? 0 : 1)) * R + row;
+    return ((c * a.ranks + rank) * 2 + (c * chunk > s ? 0 : 1)) * a.rows + row;
   };
   float mm = -INFINITY;
   for (int p = lane; p < parts; p += 32) mm = fmaxf(mm, a.part_ml[at(p) * 2]);
@@ -498,7 +388,7 @@ TreeLayout tree_layout(int B, int ctas, int rows, int D) {
   TreeLayout l;
   size_t at = 0;
   auto take = [&](size_t n) { const size_t r = at; at = (at + n + 255) / 256 * 256; return r; };
-  l.header = take((2 + static_cast<size_t>(ctas)) * 4);
+  l.header = take((2 + static_cast<size_t>(kMaxTreeCtas)) * 4);
   l.prefix = take((static_cast<size_t>(B) + 2) * 8);
   l.ml = take(static_cast<size_t>(ctas) * 2 * rows * 8);
   l.o = take(static_cast<size_t>(ctas) * 2 * rows * D * 4);
@@ -506,29 +396,43 @@ TreeLayout tree_layout(int B, int ctas, int rows, int D) {
   return l;
 }
 
-// Rows of a row tile: by the average tree, so that most units are one row tile.
-int tree_rows(int N, int B, int Hq, int Hkv) {
+// How a call is cut, from the host's sizes: the average tree's rows a KV head.
+struct TreePlan { int rows, ranks; bool wide; };
+TreePlan tree_plan(int N, int B, int Hq, int Hkv) {
   const long long avg = (static_cast<long long>(N) + B - 1) / B * (Hq / Hkv);
-  return avg <= 16 ? 16 : 32;
+  if (avg <= 16) return {16, 1, false};
+  if (avg <= 32) return {32, 1, false};
+  return {kWideRows, avg <= kWideRows ? 1 : avg <= 2 * kWideRows ? 2 : 4, true};
 }
 
 template <typename T, int D, int RT>
-cudaError_t launch_tree(TreeArgs& a, int ctas, bool may_cut, cudaStream_t s) {
-  const size_t smem = tree_smem<D, RT>(a.B);
+cudaError_t launch_narrow(TreeArgs& a, int ctas, cudaStream_t s) {
   auto kern = tree_kernel<T, D, RT>;
   cudaError_t err = set_smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(tree_smem<D, RT>(kMaxBatch)));
   if (err != cudaSuccess) return err;
-  err = launch_kernel(kern, dim3(ctas), dim3(kAThreads), smem, s, true, a);
-  if (err != cudaSuccess || !may_cut) return err;
-  const long long rows = static_cast<long long>(a.N) * a.Hq;
-  return launch_kernel(tree_join_kernel<T, D, RT * 16>, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, s, true, a);
+  return launch_kernel(kern, dim3(ctas), dim3(kAThreads), tree_smem<D, RT>(a.B), s, true, a);
 }
 
 template <typename T>
-cudaError_t launch_tree_typed(TreeArgs& a, int D, int rows, int ctas, bool may_cut, cudaStream_t s) {
-  if (D == 128) return rows == 16 ? launch_tree<T, 128, 1>(a, ctas, may_cut, s) : launch_tree<T, 128, 2>(a, ctas, may_cut, s);
-  return rows == 16 ? launch_tree<T, 64, 1>(a, ctas, may_cut, s) : launch_tree<T, 64, 2>(a, ctas, may_cut, s);
+cudaError_t launch_tree(TreeArgs& a, int D, const TreePlan& p, int sms, bool bounded_to_one_tile, cudaStream_t s) {
+  cudaError_t err;
+  if (p.wide) {
+    const int ctas = sms / p.ranks * p.ranks;
+    err = launch_tree_wide(a, std::is_same<T, __nv_bfloat16>::value, D, ctas < kMaxTreeCtas / 2 ? ctas : kMaxTreeCtas / 2 / p.ranks * p.ranks, s);
+  } else {
+    const int ctas = 2 * sms < kMaxTreeCtas ? 2 * sms : kMaxTreeCtas;
+    if (D == 128) err = p.rows == 16 ? launch_narrow<T, 128, 1>(a, ctas, s) : launch_narrow<T, 128, 2>(a, ctas, s);
+    else err = p.rows == 16 ? launch_narrow<T, 64, 1>(a, ctas, s) : launch_narrow<T, 64, 2>(a, ctas, s);
+  }
+  if (err != cudaSuccess || bounded_to_one_tile) return err;  // a unit of one tile is never cut
+  const long long rows = static_cast<long long>(a.N) * a.Hq;
+  const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
+  return D == 128 ? launch_kernel(tree_join_kernel<T, 128>, grid, dim3(128), 0, s, true, a)
+                  : launch_kernel(tree_join_kernel<T, 64>, grid, dim3(128), 0, s, true, a);
 }
+
+// CTAs that the workspace of a call has partial results for.
+int tree_part_ctas(const TreePlan& p) { return p.wide ? kMaxTreeCtas / 2 : kMaxTreeCtas; }
 
 }  // namespace
 }  // namespace gbmoe
@@ -538,7 +442,8 @@ extern "C" size_t moe_tree_attention_workspace_size(int nodes, int batch, int q_
   if (nodes < 0 || batch <= 0 || batch > kMaxBatch || q_heads <= 0 || k_heads <= 0 || q_heads % k_heads ||
       (dim != 64 && dim != 128))
     return 0;
-  return tree_layout(batch, kMaxTreeCtas, tree_rows(nodes, batch, q_heads, k_heads), dim).total;
+  const TreePlan p = tree_plan(nodes, batch, q_heads, k_heads);
+  return tree_layout(batch, tree_part_ctas(p), p.rows, dim).total;
 }
 
 extern "C" moe_status_t moe_tree_attention(const moe_tree_attention_args_t* r, void* workspace, size_t workspace_bytes,
@@ -570,10 +475,10 @@ extern "C" moe_status_t moe_tree_attention(const moe_tree_attention_args_t* r, v
     if (r->out_stride_t % 4 || r->out_stride_h % 4) return bad("output strides must be multiples of 4 elements");
     if (!aligned(r->q, 16) || !aligned(r->k_cache, 16) || !aligned(r->v_cache, 16)) return bad("q and the caches must be 16-byte aligned");
     if (!aligned(r->out, 8) || !aligned(r->tree_mask, 8)) return bad("out and tree_mask must be 8-byte aligned");
-    const int rows = tree_rows(r->nodes, r->batch, r->q_heads, r->k_heads);
+    const TreePlan p = tree_plan(r->nodes, r->batch, r->q_heads, r->k_heads);
     const int sms = num_sms_current();
     if (sms <= 0) return report_error(MOE_ERR_CUDA, "moe_tree_attention: no CUDA device");
-    const TreeLayout l = tree_layout(r->batch, kMaxTreeCtas, rows, r->dim);
+    const TreeLayout l = tree_layout(r->batch, tree_part_ctas(p), p.rows, r->dim);
     if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256))
       return report_error(MOE_ERR_WORKSPACE, "moe_tree_attention: workspace NULL, misaligned or too small");
     TreeArgs a{};
@@ -593,14 +498,13 @@ extern "C" moe_status_t moe_tree_attention(const moe_tree_attention_args_t* r, v
     a.prefix = reinterpret_cast<long long*>(ws + l.prefix);
     a.part_ml = reinterpret_cast<float*>(ws + l.ml);
     a.part_o = reinterpret_cast<float*>(ws + l.o);
-    int ctas = 2 * sms;
-    if (ctas > kMaxTreeCtas) ctas = kMaxTreeCtas;
-    // a unit of one tile is never cut
-    const bool may_cut = static_cast<long long>(r->table_width) * r->page_size > kTile;
+    a.tile = p.wide ? kWideTile : kTile;
+    a.rows = p.rows;
+    a.ranks = p.ranks;
+    const bool one_tile = static_cast<long long>(r->table_width) * r->page_size <= a.tile;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return launched("moe_tree_attention", r->dtype == MOE_DTYPE_FP16
-                                              ? launch_tree_typed<__half>(a, r->dim, rows, ctas, may_cut, s)
-                                              : launch_tree_typed<__nv_bfloat16>(a, r->dim, rows, ctas, may_cut, s));
+    return launched("moe_tree_attention", r->dtype == MOE_DTYPE_FP16 ? launch_tree<__half>(a, r->dim, p, sms, one_tile, s)
+                                                                     : launch_tree<__nv_bfloat16>(a, r->dim, p, sms, one_tile, s));
   });
 }
 
@@ -614,9 +518,13 @@ extern "C" moe_status_t moe_read_tree_status(const void* workspace, int32_t stat
     if (err == cudaSuccess) err = cudaStreamSynchronize(s);
     if (err != cudaSuccess) return launched("moe_read_tree_status", err);
     int pages = 0;
-    for (int c = 0; c < host[0] && c < kMaxTreeCtas; ++c) pages += host[2 + c];
+    bool gave_up = false;
+    for (int c = 0; c < host[0] && c < kMaxTreeCtas; ++c) {
+      if (host[2 + c] < 0) gave_up = true; else pages += host[2 + c];
+    }
     status_out[0] = host[1];
     status_out[1] = pages;
+    if (gave_up) return report_error(MOE_ERR_TIMEOUT, "moe_read_tree_status: a bounded device wait gave up");
     if (host[1] || pages)
       return report_error(MOE_ERR_BAD_IDS, "moe_read_tree_status: lengths, node offsets or cache pages out of range");
     return MOE_OK;

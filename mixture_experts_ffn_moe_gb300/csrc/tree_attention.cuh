@@ -1,0 +1,143 @@
+// Shared parts of the tree attention kernels: arguments, the line of tiles, small wrappers.
+#pragma once
+
+#include "sm100_ptx.cuh"
+#include "step_ops.cuh"
+
+namespace gbmoe {
+namespace tree {
+
+constexpr int kMaxBatch = 1024;
+constexpr int kMaxTreeCtas = 320;    // CTAs that the workspace has room for
+constexpr int kWideTile = 128;       // slots of a tile and rows of a product of the tcgen05 kernel
+constexpr int kWideRows = 256;       // rows of its row tile
+constexpr float kLazy = 8.f;         // growth of a row's maximum (in powers of two) that moves its reference
+
+struct TreeArgs {
+  const void* q;
+  const void* kc;
+  const void* vc;
+  void* out;
+  const int32_t* table;
+  const int32_t* ctx;
+  const int32_t* offs;
+  const unsigned long long* mask;  // null: a chain
+  long long q_t, q_h, o_t, o_h;
+  long long k_page, k_slot, k_head, v_page, v_slot, v_head;
+  long long table_ld;
+  int N, B, Hq, Hkv, pages, table_w;
+  int tile, rows, ranks;  // slots of a tile, rows of a CTA's row tile, CTAs that work on one range side by side
+  FastDiv page, group;
+  float scale_log2;
+  int32_t* header;    // workspace: [0] CTAs, [1] bad lengths, offsets or counts, then for every CTA its bad pages
+                      // (negative: one of its waits gave up)
+  long long* prefix;  // [B + 1] first tile of every sequence on the line, [B + 1] = tiles a group of CTAs
+  float* part_o;      // [CTAs * 2][rows][D]
+  float* part_ml;     // [CTAs * 2][rows][2]
+};
+
+__device__ __forceinline__ void ldm4(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t a, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// Words of two 16-bit elements: does either hold an infinity or NaN?
+__device__ __forceinline__ bool nonfinite2(__nv_bfloat16, uint32_t w) {
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+__device__ __forceinline__ bool nonfinite2(__half, uint32_t w) {
+  return (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+}
+
+// Committed slots and nodes of sequence b, brought into range (bad counts what had to be).
+__device__ __forceinline__ void seq_sizes(const TreeArgs& a, int b, int& ctx, int& n, int& bad) {
+  const int lo = a.offs[b], hi = a.offs[b + 1];
+  ctx = a.ctx[b];
+  n = hi - lo;
+  bad = 0;
+  const long long room = static_cast<long long>(a.table_w) * a.page.d;
+  if (lo < 0 || hi < lo || hi > a.N || n > MOE_MAX_TREE_NODES || n > room) { n = 0; bad = 1; }
+  if (ctx < 0) { ctx = 0; bad = 1; }
+  if (ctx > room - n) { ctx = static_cast<int>(room - n); bad = 1; }
+}
+
+// prefix[b] = first tile of sequence b on the line of all tiles.
+template <int THREADS>
+__device__ __forceinline__ void plan_line(const TreeArgs& a, long long* prefix, long long* scratch, int* bad) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long base = 0;
+  int nbad = 0;
+  for (int b0 = 0; b0 < a.B; b0 += THREADS) {
+    const int b = b0 + tid;
+    long long tiles = 0;
+    if (b < a.B) {
+      int ctx, n, bd;
+      seq_sizes(a, b, ctx, n, bd);
+      nbad += bd;
+      if (n > 0) {
+        const int per = a.rows * a.ranks, rt = (n * static_cast<int>(a.group.d) + per - 1) / per;
+        tiles = static_cast<long long>(a.Hkv) * rt * ((static_cast<long long>(ctx) + n + a.tile - 1) / a.tile);
+      }
+    }
+    long long incl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (lane == 31) scratch[warp] = incl;
+    __syncthreads();
+    long long before = base, all = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) before += scratch[w];
+      all += scratch[w];
+    }
+    if (b < a.B) prefix[b] = before + incl - tiles;
+    base += all;
+    __syncthreads();
+  }
+  if (tid == 0) prefix[a.B] = base;
+  *bad = nbad;
+  __syncthreads();
+}
+
+// A CTA group's piece of one unit: sequence, KV head, row tile, and the tiles [k0, k1) of the unit's kt.
+struct Piece {
+  int b, ctx, n, head, row0, rows, node0, k0, k1, kt;
+};
+__device__ __forceinline__ Piece piece_at(const TreeArgs& a, const long long* prefix, long long pos, long long end, int rank) {
+  Piece u;
+  int lo = 0, hi = a.B;  // prefix[lo] <= pos < prefix[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= pos) lo = mid; else hi = mid;
+  }
+  u.b = lo;
+  int bad;
+  seq_sizes(a, u.b, u.ctx, u.n, bad);
+  u.kt = (u.ctx + u.n + a.tile - 1) / a.tile;
+  const int group = a.group.d, per = a.rows * a.ranks, rt_n = (u.n * group + per - 1) / per;
+  const long long rel = pos - prefix[u.b];
+  const int unit = static_cast<int>(rel / u.kt);
+  u.k0 = static_cast<int>(rel - static_cast<long long>(unit) * u.kt);
+  u.k1 = static_cast<int>(end - pos < u.kt - u.k0 ? u.k0 + (end - pos) : u.kt);
+  u.head = unit / rt_n;
+  u.row0 = (unit - u.head * rt_n) * per + rank * a.rows;
+  u.rows = max(0, min(a.rows, u.n * group - u.row0));
+  u.node0 = a.offs[u.b];
+  return u;
+}
+
+// Launches the tcgen05 kernel (tree_attention_wide.cu) on `ctas` CTAs, one an SM.
+cudaError_t launch_tree_wide(const TreeArgs& a, bool bf16, int D, int ctas, cudaStream_t s);
+
+}  // namespace tree
+}  // namespace gbmoe

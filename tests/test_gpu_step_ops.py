@@ -247,6 +247,14 @@ def _dev(c):
     ([2500, 130, 1], [16, 24, 2], 5, 1, 128, 256, FP, "tree", False),
     ([700] * 40, [3] * 40, 4, 4, 64, 32, BF, None, False),
     ([12000, 1], [2, 1], 8, 8, 128, 128, FP, "random", False),
+    # wide trees: one and two products of 128 rows, several row tiles, ragged ones, tiles of 128 slots and their edges
+    ([0], [33], 1, 1, 128, 16, BF, "tree", False),
+    ([127], [1], 64, 1, 64, 16, BF, None, False),
+    ([126, 128, 129, 0, 300], [64, 60, 63, 1, 50], 4, 1, 128, 16, FP, "random", True),
+    ([5000, 0, 40, 250], [64, 64, 2, 33], 32, 2, 128, 7, BF, "tree", False),
+    ([3000], [64], 48, 2, 64, 64, FP, "tree", False),
+    ([257] * 9, [20] * 9, 12, 3, 64, 1, BF, "tree", False),
+    ([20000], [40], 8, 1, 128, 256, BF, None, False),
 ])
 def test_tree_attention(ctx, counts, hq, hk, D, page, dt, masks, hf):
     case = make_tree(ctx, counts, hq, hk, D, page, dt, 11 + len(ctx) + D, masks, hf)
@@ -266,11 +274,12 @@ def test_tree_rows_that_see_nothing_and_empty_sequences():
     assert (got[0] == 0).all() and (got[3] == 0).all()
 
 
+@pytest.mark.parametrize("hq", [4, 64])
 @pytest.mark.parametrize("dt,value", [(BF, float("nan")), (BF, float("inf")), (FP, float("-inf"))])
-def test_tree_hidden_slots_do_not_leak(dt, value):
+def test_tree_hidden_slots_do_not_leak(dt, value, hq):
     """Node 1 holds infinities and NaN; nodes that do not see it are as without, those that see it get them."""
-    ctx, counts, D, page = [70], [5], 128, 16
-    case = list(make_tree(ctx, counts, 4, 2, D, page, dt, 5, "tree"))
+    ctx, counts, D, page, half = [70], [5], 128, 16, hq // 2
+    case = list(make_tree(ctx, counts, hq, 2, D, page, dt, 5, "tree"))
     case[6] = ancestors([-1, -1, 0, 1, 2])
     q, kc, vc, table = case[:4]
     slot = 71
@@ -281,13 +290,14 @@ def test_tree_hidden_slots_do_not_leak(dt, value):
     for j in (0, 2, 4):
         close(got[j], ref[j], bound[j])
     for j in (1, 3):
-        assert not got[j, :2, ::3].isfinite().any()  # first KV head: keys are finite, the value's elements are not
-        close(got[j, :2, 1::3], ref[j, :2, 1::3], bound[j, :2, 1::3])
-        close(got[j, :2, 2::3], ref[j, :2, 2::3], bound[j, :2, 2::3])
+        assert not got[j, :half, ::3].isfinite().any()  # first KV head: keys are finite, the value's elements are not
+        close(got[j, :half, 1::3], ref[j, :half, 1::3], bound[j, :half, 1::3])
+        close(got[j, :half, 2::3], ref[j, :half, 2::3], bound[j, :half, 2::3])
 
 
-def test_tree_attention_large_scores_and_scale():
-    case = make_tree([300], [6], 4, 1, 128, 16, BF, 9, "tree")
+@pytest.mark.parametrize("hq", [4, 32])
+def test_tree_attention_large_scores_and_scale(hq):
+    case = make_tree([300], [6], hq, 1, 128, 16, BF, 9, "tree")
     q = case[0] * 30
     close(run_tree(q, *case[1:], scale=0.5), *tree_ref(q, *case[1:], 0.5))
     close(run_tree(q, *case[1:], scale=-0.01), *tree_ref(q, *case[1:], -0.01))
@@ -323,19 +333,21 @@ def test_tree_attention_strided_tensors():
     assert (out[:, 0] == 0).all() and (out[:, 5] == 0).all() and (out[:, :, 64:] == 0).all()
 
 
-def test_tree_attention_reports_and_leaves_out_bad_pages():
-    case = list(make_tree([100, 30], [2, 2], 2, 1, 64, 16, BF, 13, "tree"))
+@pytest.mark.parametrize("hq", [2, 64])
+def test_tree_attention_reports_and_leaves_out_bad_pages(hq):
+    case = list(make_tree([100, 30], [2, 2], hq, 1, 64, 16, BF, 13, "tree"))
     case[3][0, 2] = 9999
     case[3][1, 0] = -5
-    ws = torch.empty(gbmoe.moe_tree_attention_workspace_size(4, 2, 2, 1, 64), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(gbmoe.moe_tree_attention_workspace_size(4, 2, hq, 1, 64), dtype=torch.uint8, device="cuda")
     close(run_tree(*case, workspace=ws), *tree_ref(*case, 64 ** -0.5))
     seqs, pages, st = gbmoe.moe_read_tree_status(ws)
     assert seqs == 0 and pages >= 32 and st == 6
 
 
-def test_tree_attention_bad_lengths_are_counted():
-    case = list(make_tree([100, 30], [2, 2], 2, 1, 64, 16, BF, 14, "tree"))
-    ws = torch.empty(gbmoe.moe_tree_attention_workspace_size(4, 2, 2, 1, 64), dtype=torch.uint8, device="cuda")
+@pytest.mark.parametrize("hq", [2, 64])
+def test_tree_attention_bad_lengths_are_counted(hq):
+    case = list(make_tree([100, 30], [2, 2], hq, 1, 64, 16, BF, 14, "tree"))
+    ws = torch.empty(gbmoe.moe_tree_attention_workspace_size(4, 2, hq, 1, 64), dtype=torch.uint8, device="cuda")
     good = run_tree(*case, workspace=ws)
     case[4] = [100, 10 ** 9]  # longer than its table: shortened
     got = run_tree(*case, workspace=ws)
@@ -347,14 +359,15 @@ def test_tree_attention_bad_lengths_are_counted():
     assert torch.equal(got[:2], good[:2])
 
 
-def test_tree_attention_in_a_graph_serves_other_lengths():
-    long, short = make_tree([300], [6], 4, 2, 64, 16, BF, 15, "tree"), make_tree([20], [6], 4, 2, 64, 16, BF, 16, "tree")
+@pytest.mark.parametrize("hq", [4, 40])
+def test_tree_attention_in_a_graph_serves_other_lengths(hq):
+    long, short = make_tree([300], [6], hq, 2, 64, 16, BF, 15, "tree"), make_tree([20], [6], hq, 2, 64, 16, BF, 16, "tree")
     table = torch.full((1, 20), -1, dtype=torch.int32, device="cuda")
     ctx, offs = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.tensor([0, 6], dtype=torch.int32, device="cuda")
-    q, mask = torch.zeros(6, 4, 64, dtype=BF, device="cuda"), torch.zeros(6, dtype=torch.int64, device="cuda")
+    q, mask = torch.zeros(6, hq, 64, dtype=BF, device="cuda"), torch.zeros(6, dtype=torch.int64, device="cuda")
     kc, vc = (torch.zeros(30, 16, 2, 64, dtype=BF, device="cuda") for _ in range(2))
     out = torch.zeros_like(q)
-    ws = torch.empty(gbmoe.moe_tree_attention_workspace_size(6, 1, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(gbmoe.moe_tree_attention_workspace_size(6, 1, hq, 2, 64), dtype=torch.uint8, device="cuda")
 
     def load(case):
         q.copy_(case[0])
