@@ -214,6 +214,10 @@ cudaError_t launch_combine(const __nv_bfloat16* y, const int32_t* inv_pos, int M
 // 2D row-major tensor [outer, inner] of `esize`-byte elements, TMA box [box_outer, box_inner].
 bool encode_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* base, uint64_t inner,
                     uint64_t outer, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
+// A paged cache of 16-bit elements as a tensor [pages, heads, page_size, dim] (strides in elements), 128-byte-swizzled
+// boxes of box_slots rows of one page and head.  False where the strides do not fit a tensor map.
+bool encode_tmap_cache(CUtensorMap* m, const void* base, int dim, int page_size, int heads, int pages, long long slot,
+                       long long head, long long page, int box_dim, int box_slots);
 cudaError_t launch_requant_rows(const void* h, const uint32_t* hmax, const int32_t* num_post, int cap, int I,
                                 __half* hq, float* sh, int num_sms, cudaStream_t s);
 // tcgen05 path, FP8 and INT4 weights: brings every position's h blocks to the row frame (the largest

@@ -708,6 +708,22 @@ bool encode_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, int esize, const voi
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tmap_cache(CUtensorMap* m, const void* base, int dim, int page_size, int heads, int pages, long long slot,
+                       long long head, long long page, int box_dim, int box_slots) {
+  EncodeTiledFn fn = encode_fn();
+  const long long limit = 1LL << 39;  // strides in elements: below 2^40 bytes
+  if (!fn || slot <= 0 || head <= 0 || page <= 0 || slot >= limit || head >= limit || page >= limit || pages <= 0) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(page_size),
+                              static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(slot) * 2, static_cast<cuuint64_t>(head) * 2,
+                                 static_cast<cuuint64_t>(page) * 2};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(box_dim), static_cast<cuuint32_t>(box_slots), 1, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int WK, bool GATED>
 static cudaError_t launch_gemm(const PrefillArgs& a, const void* w, uint64_t w_rows, const void* b, uint64_t b_rows,
                                int num_sms, cudaStream_t s) {

@@ -28,6 +28,7 @@ struct TreeArgs {
   int N, B, Hq, Hkv, pages, table_w;
   int tile, rows, ranks;  // slots of a tile, rows of a CTA's row tile, CTAs that work on one range side by side
   FastDiv page, group;
+  int box;                // slots of a page that one TMA copy brings (0: cp.async)
   float scale_log2;
   int32_t* header;    // workspace: [0] CTAs, [1] bad lengths, offsets or counts, then for every CTA its bad pages
                       // (negative: one of its waits gave up)

@@ -9,8 +9,10 @@
 //   P_i = 2^(S_i * scale - m_i), one thread a row, written back over S_i as 16-bit values
 //   O_i += P_i V (P_i from tensor memory, V from shared memory with its rows as the K dimension)
 // The products of one i run while the other's softmax does.  Tensor memory holds S_0, S_1, O_0, O_1 (4 x 128
-// columns for D = 128).  Roles: 2 x 4 softmax warps, 4 loader warps (cp.async into the 128-byte-swizzled layout,
-// slot by slot through the block table, so any page size and stride works), one thread that issues the products.
+// columns for D = 128).  Roles: 2 x 4 softmax warps, one thread that issues the products, and the loaders: where pages
+// hold a multiple of 8 slots one warp whose lanes each bring a page's part of a tile by TMA, else 4 warps with
+// cp.async, slot by slot (any page size and stride).  The latter spend about 4,600 cycles on the instructions of a
+// tile, twice what its products take; the TMA loader is not seen.
 //
 // CTAs whose row tiles belong to the same cache range (up to 4) walk over it side by side, so that HBM delivers it
 // once and L2 the rest.  Every wait is bounded: a role that gives up marks the CTA and all leave.
@@ -94,8 +96,9 @@ __device__ __forceinline__ uint32_t visible(uint32_t ok, int first, int ctx, uns
   return d <= -64 ? 0u : ok & static_cast<uint32_t>(bits >> -d);
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(TreeArgs a) {
+template <typename T, int D, bool TMA>
+__global__ void __launch_bounds__(kThreads, 1)
+    tree_wide_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   using C = WideCfg<D>;
   constexpr int CH = D / 8, HALF = 128 * 128;  // 16-byte chunks of a row; bytes of 64 columns of a tile
   extern __shared__ unsigned char raw[];
@@ -111,8 +114,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(TreeArgs a) {
   pdl_trigger();
   if (tid == 0) {
     for (int i = 0; i < C::NS; ++i) {
-      mbar_init(&sm.k_full[i], 128);
-      mbar_init(&sm.v_full[i], 128);
+      mbar_init(&sm.k_full[i], TMA ? 1 : 128);
+      mbar_init(&sm.v_full[i], TMA ? 1 : 128);
       mbar_init(&sm.k_empty[i], 1);
       mbar_init(&sm.v_empty[i], 1);
     }
@@ -267,6 +270,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(TreeArgs a) {
                 *reinterpret_cast<uint4*>(v + (z >> 3) * HALF + r * 128 + ((z & 7) << 4)) = make_uint4(0, 0, 0, 0);
             }
           }
+          if constexpr (TMA) {  // rows of the last page past the sequence's end hold anything
+            for (int c = hi * CH + r_in; c < 128 * CH; c += 128) {
+              const int r = c / CH, ch = c % CH;
+              *reinterpret_cast<uint4*>(v + (ch >> 3) * HALF + r * 128 + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
+            }
+          }
           fence_proxy_async_smem();
         }
         tmem_st_wait();
@@ -323,10 +332,64 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(TreeArgs a) {
       ++piece;
     }
   } else if (warp < 12) {
-    // ---------------------------------------------------------------- loaders: 32 slots of every tile a warp
+    // ---------------------------------------------------------------- loaders
     regs_dec<64>();
+    if constexpr (TMA) {
+      if (warp == 8) {  // lane j: the part of a tile in its j-th run of `box` slots
+        int n = 0, bad = 0, k_sent = 0, v_sent = 0;
+        bool fine = true;
+        const int boxes = 128 / a.box;
+        for (long long pos = first; pos < end && fine;) {
+          const Piece u = piece_at(a, prefix, pos, end, rank);
+          pos += u.k1 - u.k0;
+          if (u.rows == 0) continue;
+          const int32_t* table = a.table + u.b * a.table_ld;
+          const int L = u.ctx + u.n;
+          for (int it = u.k0; it < u.k1 && fine; ++it, ++n) {
+            int page = -1, at = 0;  // page -1 is outside the tensor: zeros
+            const int slot = it * 128 + lane * a.box;
+            if (lane < boxes && slot < L) {
+              const int pi = div_by(slot, a.page);
+              at = slot - pi * a.page.d;
+              page = __ldg(table + pi);
+              if (page < 0 || page >= a.pages) { page = -1; bad += min(a.box, L - slot); }
+            }
+            uint32_t ok[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int s = w * 32 + lane;
+              ok[w] = __ballot_sync(0xffffffffu, __shfl_sync(0xffffffffu, page, s / a.box) >= 0 && it * 128 + s < L);
+            }
+            const int st = n % C::NS;
+            const uint32_t parity = ((n / C::NS) & 1) ^ 1;
+#pragma unroll
+            for (int kv = 0; kv < 2 && fine; ++kv) {
+              if (!(fine = warp_wait(kv ? &sm.v_empty[st] : &sm.k_empty[st], parity))) break;
+              uint64_t* full = kv ? &sm.v_full[st] : &sm.k_full[st];
+              if (lane == 0) {
+                if (kv == 0) *reinterpret_cast<uint4*>(sm.ok[n & 7]) = make_uint4(ok[0], ok[1], ok[2], ok[3]);
+                mbar_arrive_expect_tx(full, C::kTileBytes);
+              }
+              if (kv) ++v_sent; else ++k_sent;
+              __syncwarp();
+              const uint32_t dst = smem_addr((kv ? vs : ks) + st * C::kTileBytes) + lane * a.box * 128;
+              if (lane < boxes)
+#pragma unroll
+                for (int h = 0; h < D / 64; ++h) tma_load_4d(dst + h * HALF, kv ? &mv : &mk, full, h * 64, at, u.head, page);
+            }
+          }
+        }
+        if (!fine && lane == 0) {  // copies on their way land before the CTA goes
+          int none = 0;
+          for (int t = max(0, k_sent - C::NS); t < k_sent; ++t) mbar_wait(&sm.k_full[t % C::NS], (t / C::NS) & 1, &none, nullptr, kLimit);
+          for (int t = max(0, v_sent - C::NS); t < v_sent; ++t) mbar_wait(&sm.v_full[t % C::NS], (t / C::NS) & 1, &none, nullptr, kLimit);
+        }
+        bad = __reduce_add_sync(0xffffffffu, bad);
+        if (lane == 0 && bad) atomicAdd(&sm.bad_pages, bad);
+      }
+    } else {
     const int lw = warp - 8;
-    int n = 0, bad = 0;
+    int n = 0, bad = 0, sent = 0;  // loads announced so far
     bool fine = true;
     auto arrive_load = [&](int q) {  // load q: K of tile q / 2, or its V
       fence_proxy_async_smem();
@@ -353,7 +416,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(TreeArgs a) {
         const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          fine = warp_wait(kv ? &sm.v_empty[n % C::NS] : &sm.k_empty[n % C::NS], ((n / C::NS) & 1) ^ 1);
+          uint64_t* empty = kv ? &sm.v_empty[n % C::NS] : &sm.k_empty[n % C::NS];
+          const uint32_t parity = ((n / C::NS) & 1) ^ 1;
+          if (!__all_sync(0xffffffffu, mbar_try_wait(empty, parity))) {
+            // no room: announce all that is on its way before waiting, since the room may depend on it
+            cp_wait<0>();
+            for (; sent < 2 * n + kv; ++sent) arrive_load(sent);
+            fine = warp_wait(empty, parity);
+          }
           if (!fine) break;
           if (kv == 0 && lane == 0) sm.ok[n & 7][lw] = ok;
           const uint32_t dst = smem_addr((kv ? vs : ks) + (n % C::NS) * C::kTileBytes);
@@ -370,15 +440,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(TreeArgs a) {
           }
           cp_commit();
           const int q = 2 * n + kv;
-          if (q >= C::LAG) { cp_wait<C::LAG>(); arrive_load(q - C::LAG); }
+          if (sent <= q - C::LAG) {
+            cp_wait<C::LAG>();
+            for (; sent <= q - C::LAG; ++sent) arrive_load(sent);
+          }
         }
       }
     }
     cp_wait<0>();
     if (fine)
-      for (int q = max(2 * n - C::LAG, 0); q < 2 * n; ++q) arrive_load(q);
+      for (; sent < 2 * n; ++sent) arrive_load(sent);
     bad = __reduce_add_sync(0xffffffffu, bad);
     if (lane == 0 && bad) atomicAdd(&sm.bad_pages, bad);
+    }
   } else {
     // ---------------------------------------------------------------- products: one thread issues
     regs_dec<64>();
@@ -453,11 +527,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_wide_kernel(TreeArgs a) {
 }
 
 template <typename T, int D>
-cudaError_t launch(const TreeArgs& a, int ctas, cudaStream_t s) {
-  auto kern = tree_wide_kernel<T, D>;
+cudaError_t launch(TreeArgs a, int ctas, cudaStream_t s) {
+  CUtensorMap mk{}, mv{};
+  // runs of slots that lie in one page and stand on 8-row groups of the swizzled tile
+  a.box = 128;
+  while (a.box > 1 && a.page.d % a.box) a.box /= 2;
+  if (a.box < 8 || !encode_tmap_cache(&mk, a.kc, D, a.page.d, a.Hkv, a.pages, a.k_slot, a.k_head, a.k_page, 64, a.box) ||
+      !encode_tmap_cache(&mv, a.vc, D, a.page.d, a.Hkv, a.pages, a.v_slot, a.v_head, a.v_page, 64, a.box))
+    a.box = 0;
+  auto kern = a.box ? tree_wide_kernel<T, D, true> : tree_wide_kernel<T, D, false>;
   cudaError_t err = set_smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(wide_smem<D>(kMaxBatch)));
   if (err != cudaSuccess) return err;
-  return launch_kernel(kern, dim3(ctas), dim3(kThreads), wide_smem<D>(a.B), s, true, a);
+  return launch_kernel(kern, dim3(ctas), dim3(kThreads), wide_smem<D>(a.B), s, true, a, mk, mv);
 }
 
 }  // namespace
