@@ -14,8 +14,10 @@
 // threshold is one of integers: FP64 sums would be equally exact but run at a sixtieth of the integer rate here.
 //
 // Bound: the one row (two with q) of the vocabulary that is sampled from; everything else is a gather of at most
-// 64 probabilities.  A cluster of CTAs shares a sequence's row: each sums a contiguous part, the parts meet
-// through distributed shared memory, and the warp whose part holds the threshold reads it once more.
+// 64 probabilities.  In practice a chain of dependent reads: offsets, nodes, their probabilities, the row, and the
+// part of it that holds the threshold.  A cluster of CTAs shares a sequence's row, a warp takes tiles of 1024
+// tokens with all of its loads in flight, the CTAs' sums meet through distributed shared memory, and one warp
+// reads the one tile again in which the running sum passes the threshold.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -26,9 +28,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kVThreads = 512;
+constexpr int kVThreads = 256;   // two CTAs an SM at about 120 registers
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kVTile = 1024;     // tokens of a tile: 32 a lane
+constexpr int kVTiles = 2048;    // tiles of a CTA at most
 
 struct VerifyArgs {
   const float* target;  // [N + B, V], row stride ldt
@@ -75,6 +79,32 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
   return v;
 }
 
+// A lane's 32 weights of the tile at `base`, all loads in flight: VEC neighbours of every 32 * VEC tokens.  fs: the
+// plain sum of p, to tell rows that are no probabilities.
+template <int VEC>
+__device__ __forceinline__ void load_tile(const float* p, const float* q, int base, int V, int lane, uint64_t (&w)[32], float& fs) {
+  float a[32], b[32];
+#pragma unroll
+  for (int i = 0; i < 32; i += VEC) {
+    const int at = base + (i / VEC * 32 + lane) * VEC;
+    if constexpr (VEC == 4) {
+      const bool in = at + 3 < V;  // V is a multiple of 4
+      const float4 x = in ? __ldg(reinterpret_cast<const float4*>(p + at)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float4 y = in && q ? __ldg(reinterpret_cast<const float4*>(q + at)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      a[i] = x.x; a[i + 1] = x.y; a[i + 2] = x.z; a[i + 3] = x.w;
+      b[i] = y.x; b[i + 1] = y.y; b[i + 2] = y.z; b[i + 3] = y.w;
+    } else {
+      a[i] = at < V ? __ldg(p + at) : 0.f;
+      b[i] = at < V && q ? __ldg(q + at) : 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    w[i] = weight(a[i], b[i], q != nullptr);
+    fs += a[i] > 0.f ? fminf(a[i], 1.f) : 0.f;
+  }
+}
+
 struct Shared {
   int tok[64], par[64];
   float p[64];
@@ -88,7 +118,8 @@ struct Shared {
   int found;
 };
 
-__global__ void __launch_bounds__(kVThreads) verify_kernel(VerifyArgs a) {
+template <int VEC>
+__global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyArgs a) {
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = cluster.num_blocks(), rank = cluster.block_rank();
@@ -162,28 +193,31 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(VerifyArgs a) {
   const float* prow = a.target + (row0 + stop + 1) * a.ldt;
   const bool has_q = a.draft && stop + 1 < n;
   const float* qrow = has_q ? a.draft + (lo + static_cast<long long>(stop) + 1) * a.ldd : nullptr;
-  const int per_warp = ((a.V + C * kVWarps - 1) / (C * kVWarps) + 31) / 32 * 32;
-  const int ws = min(static_cast<long long>(a.V), static_cast<long long>(rank * kVWarps + warp) * per_warp);
-  const int we = min(a.V, ws + per_warp);
+  extern __shared__ uint64_t tile_sum[];  // [tiles of this CTA]
+  const int tiles = (a.V + kVTile - 1) / kVTile, per_cta = (tiles + C - 1) / C;
+  const int tile0 = min(tiles, rank * per_cta), my_tiles = min(tiles, tile0 + per_cta) - tile0;
   int next = -1;
-  // children: 1 = the residual (draft's share, or the refused children, taken away), 0 = the plain row where
-  // the residual has no weight left
+  // residual: 1 = the draft's share, or the refused children, taken away; 0 = the plain row where nothing is left
   for (int residual = 1; !bad && residual >= 0 && next < 0; --residual) {
-    uint64_t s = 0;
+    const bool use_q = has_q && residual;
     float fs = 0.f;
-#pragma unroll 4
-    for (int i = ws + lane; i < we; i += 32) {
-      const float p = prow[i], qq = has_q && residual ? qrow[i] : 0.f;
-      s += weight(p, qq, has_q && residual);
-      fs += p > 0.f ? fminf(p, 1.f) : 0.f;
+    uint64_t mine = 0;  // lane 0: the warp's tiles
+    for (int t = warp; t < my_tiles; t += kVWarps) {
+      uint64_t w[32];
+      uint64_t sum = 0;
+      load_tile<VEC>(prow, use_q ? qrow : nullptr, (tile0 + t) * kVTile, a.V, lane, w, fs);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum += w[i];
+      if (!a.draft && residual)
+        for (int j = lane; j < n; j += 32)
+          if (sh.par[j] == stop && !sh.again[j] && sh.tok[j] / kVTile == tile0 + t) sum -= fixed56(sh.p[j]);
+      sum = warp_sum64(sum);
+      if (lane == 0) tile_sum[t] = sum;
+      mine += sum;
     }
-    if (!a.draft && residual)
-      for (int j = lane; j < n; j += 32)
-        if (sh.par[j] == stop && !sh.again[j] && sh.tok[j] >= ws && sh.tok[j] < we) s -= fixed56(sh.p[j]);
-    s = warp_sum64(s);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) fs += __shfl_xor_sync(0xffffffffu, fs, o);
-    if (lane == 0) { sh.warp_tot[warp] = s; sh.warp_f[warp] = fs; }
+    if (lane == 0) { sh.warp_tot[warp] = mine; sh.warp_f[warp] = fs; }
     __syncthreads();
     if (tid < C) {  // this CTA's total into slot `rank` of every CTA of the cluster
       uint64_t tot = 0;
@@ -203,20 +237,12 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(VerifyArgs a) {
     }
     if (!(f <= 128.f)) break;  // not probabilities: 56 bits would overflow
     if (total != 0) {
-      for (int w = 0; w < warp; ++w) before += sh.warp_tot[w];
       // floor(u * total) for u in [0, 1): x is the first token whose running sum is above it
       const uint64_t level = __umul64hi(fraction64(a.last[b]), total);
-      if (level >= before && level < before + sh.warp_tot[warp]) {  // one warp of the cluster
-        for (int i0 = ws; i0 < we; i0 += 32) {
-          const int i = i0 + lane;
-          uint64_t w = 0;
-          if (i < we) {
-            w = weight(prow[i], has_q && residual ? qrow[i] : 0.f, has_q && residual);
-            if (!a.draft && residual)
-              for (int j = 0; j < n; ++j)
-                if (sh.par[j] == stop && sh.tok[j] == i) w = 0;
-          }
-          uint64_t run = w;
+      if (warp == 0 && level >= before && level < before + sh.cta_tot[rank]) {  // in this CTA's part
+        int t = 0;
+        for (int t0 = 0; t0 < my_tiles; t0 += 32) {  // the tile
+          uint64_t run = t0 + lane < my_tiles ? tile_sum[t0 + lane] : 0;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
             const uint64_t up = __shfl_up_sync(0xffffffffu, run, o);
@@ -224,11 +250,51 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(VerifyArgs a) {
           }
           const unsigned hit = __ballot_sync(0xffffffffu, before + run > level);
           if (hit) {
-            if (lane == 0) {
-              const int x = i0 + __ffs(hit) - 1;
+            const int l = __ffs(hit) - 1;
+            t = t0 + l;
+            const uint64_t upto = __shfl_sync(0xffffffffu, run, l ? l - 1 : 0);
+            before += l ? upto : 0;
+            break;
+          }
+          before += __shfl_sync(0xffffffffu, run, 31);
+        }
+        uint64_t w[32];
+        const int base = (tile0 + t) * kVTile;
+        load_tile<VEC>(prow, use_q ? qrow : nullptr, base, a.V, lane, w, fs);
+        if (!a.draft && residual)
+          for (int j = 0; j < n; ++j)
+            if (sh.par[j] == stop && sh.tok[j] / kVTile == tile0 + t) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (base + (i / VEC * 32 + lane) * VEC + i % VEC == sh.tok[j]) w[i] = 0;
+            }
+        // tokens in order: groups of 32 * VEC, in them VEC a lane
+        bool found = false;
+#pragma unroll
+        for (int i0 = 0; i0 < 32; i0 += VEC) {
+          uint64_t own = 0;
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) own += w[i0 + i];
+          uint64_t run = own;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t up = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += up;
+          }
+          const unsigned hit = found ? 0u : __ballot_sync(0xffffffffu, before + run > level);
+          if (hit) {
+            found = true;
+            if (lane == __ffs(hit) - 1) {
+              uint64_t at = before + run - own;
+              int x = base + (i0 / VEC * 32 + lane) * VEC;
+              bool here = false;
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) {
+                at += w[i0 + i];
+                if (!here && at > level) { here = true; x += i; }
+              }
               cluster.map_shared_rank(&sh, 0)->found = x;
             }
-            break;
           }
           before += __shfl_sync(0xffffffffu, run, 31);
         }
@@ -269,7 +335,7 @@ extern "C" moe_status_t moe_verify_draft(const float* target_probs, int64_t targ
     if (batch < 0 || nodes < 0 || vocab <= 0 || max_nodes < 0) return bad("sizes must be positive");
     if (max_nodes > MOE_MAX_TREE_NODES)
       return report_error(MOE_ERR_UNSUPPORTED, "moe_verify_draft: more than MOE_MAX_TREE_NODES nodes a sequence");
-    if (vocab > (1 << 24) || batch > (1 << 20))
+    if (vocab > kVTile * kVTiles || batch > (1 << 20))
       return report_error(MOE_ERR_UNSUPPORTED, "moe_verify_draft: problem too large");
     if (batch == 0) return MOE_OK;
     if (!target_probs || !node_offsets || !coins || !last_coins || !out_tokens || !accepted || (max_nodes && !path) ||
@@ -282,10 +348,15 @@ extern "C" moe_status_t moe_verify_draft(const float* target_probs, int64_t targ
     const int sms = num_sms_current();
     if (sms <= 0) return report_error(MOE_ERR_CUDA, "moe_verify_draft: no CUDA device");
     int C = 1;
-    while (C < kMaxCluster && 2 * C * batch <= 4 * sms && vocab > 2 * C * kVThreads) C *= 2;
+    const int tiles = (vocab + kVTile - 1) / kVTile;
+    while (C < kMaxCluster && 2 * C * batch <= 2 * sms && tiles > C * kVWarps / 2) C *= 2;
+    // 16-byte loads where every row starts on 16 bytes
+    const bool vec = vocab % 4 == 0 && target_stride % 4 == 0 && aligned(target_probs, 16) &&
+                     (!draft_probs || (draft_stride % 4 == 0 && aligned(draft_probs, 16)));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(batch) * C);
     cfg.blockDim = dim3(kVThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>((tiles + C - 1) / C) * 8;
     cfg.stream = reinterpret_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -296,6 +367,6 @@ extern "C" moe_status_t moe_verify_draft(const float* target_probs, int64_t targ
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return launched("moe_verify_draft", cudaLaunchKernelEx(&cfg, verify_kernel, a));
+    return launched("moe_verify_draft", vec ? cudaLaunchKernelEx(&cfg, verify_kernel<4>, a) : cudaLaunchKernelEx(&cfg, verify_kernel<1>, a));
   });
 }

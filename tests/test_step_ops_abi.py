@@ -126,7 +126,7 @@ def test_verify_refusals(lib):
     assert verify(lib, B=-1) == 1
     assert verify(lib, V=0) == 1
     assert verify(lib, mx=65) == 2
-    assert verify(lib, V=1 << 25) == 2
+    assert verify(lib, V=1 << 25, ts=1 << 25) == 2
     assert verify(lib, t=None) == 1
     assert verify(lib, acc=None) == 1
     assert verify(lib, d=P, ds=100, par=P) == 1                 # draft probabilities need a chain
