@@ -521,10 +521,11 @@ moe_status_t moe_rope(const moe_rope_args_t* args, moe_stream_t stream);
  * as fp16 in a power-of-two frame per row and 128 columns (exact to 2^-39 of the
  * block's largest value), sums are fp32, y is rounded once.  Made for the few
  * rows of a decode step (M up to 64 or so); any M is accepted.
- *   workspace    moe_linear_int4_workspace_size(M, K, group) bytes, 256-byte
- *                aligned; 0 bytes (NULL) for M <= 8 unless K is above 10,000 or so
+ *   workspace    moe_linear_int4_workspace_size(...) bytes, 256-byte aligned; 0
+ *                bytes (NULL) for M <= 8 unless K is above 12,000.  Where one is
+ *                used, moe_read_status(workspace) tells whether a device wait gave up.
  */
-size_t moe_linear_int4_workspace_size(int M, int K, int group);
+size_t moe_linear_int4_workspace_size(int M, int N, int K, int group, int gated);
 moe_status_t moe_linear_int4(int dtype, const void* x, int64_t x_stride, const uint8_t* w, const float* w_scale,
                              int M, int N, int K, int group, int gated, void* y, int64_t y_stride,
                              void* workspace, size_t workspace_bytes, moe_stream_t stream);

@@ -253,6 +253,7 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+constexpr int kMaxSms = 152;  // of a GB300
 // SMs of the current device (0 if it cannot be asked).
 int num_sms_current();
 

@@ -13,8 +13,7 @@
 // lies in [2^14, 2^15), so what fp16 rounds off is below 2^-39 of it, far below the fp32 sums.
 //  * Up to 8 tokens whose x fits: every CTA (persistent, one an SM) does that itself into shared memory, where x
 //    stays for all of its tiles: one launch.
-//  * Otherwise a first kernel writes the pieces to the workspace, and each warp brings those of its next blocks
-//    into a cp.async ring of its own (a lane reads back what it fetched): no barriers and any M and K.
+//  * Otherwise a first kernel writes them to the workspace for the tcgen05 kernel (linear_int4_wide.cu).
 //
 // Expansion.  It is the integer pipe that limits this kernel beside HBM, so a pair of codes takes one LOP3 (and a
 // word one shift): the biased code u = q + 8 stands alone in an fp16 as a subnormal, u * 2^-24, or 16 u * 2^-24
@@ -29,42 +28,14 @@
 
 #include <type_traits>
 
-#include "step_ops.cuh"
+#include "linear_int4.cuh"
 
 namespace gbmoe {
+namespace linear {
 namespace {
 
 constexpr int kKBlock = 128;
 constexpr size_t kLinearSmem = 224 * 1024;
-
-struct LinearArgs {
-  const void* x;       // [M, K], row stride ldx
-  const uint8_t* w;    // [N or 2N, K / 2]
-  const float* scale;  // [N or 2N, K / group]
-  void* y;             // [M, N], row stride ldy
-  long long ldx, ldy;
-  int M, N, K, gated, bf16;
-  int wr;              // warps that share a tile's blocks in the row direction (the others split K)
-  // x as the products take it, tokens in tiles of 8, nt tiles (shared memory or workspace)
-  int nt;
-  uint4* xf;           // [blocks][nt][4][32]
-  float* sums;         // [blocks][P + 1][nt * 8]: -8 * 2^-24 * the groups' sums, then 2^(frame + 12)
-  float* odd;          // [blocks][4] not 0 where a block holds infinities or NaN
-};
-
-// Pairs (k0,k4) (k1,k5) (k2,k6) (k3,k7) of a word's biased codes: u, 16 u, u, 16 u in units of 2^-24.
-__device__ __forceinline__ void expand8(uint32_t w, uint32_t r[4]) {
-  const uint32_t v = w >> 8;
-  r[0] = lop3_sel_xor(w, 0x000f000fu, 0x00080008u);
-  r[1] = lop3_sel_xor(w, 0x00f000f0u, 0x00800080u);
-  r[2] = lop3_sel_xor(v, 0x000f000fu, 0x00080008u);
-  r[3] = lop3_sel_xor(v, 0x00f000f0u, 0x00800080u);
-}
-// The codes themselves, q or 16 q in units of 2^-24 (exact).
-__device__ __forceinline__ uint32_t unbias2(uint32_t v, uint32_t bias) {
-  const __half2 q = __hsub2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&bias));
-  return *reinterpret_cast<const uint32_t*>(&q);
-}
 
 template <int RT> constexpr int kInFlight = RT == 1 ? 4 : 2;  // blocks in flight a warp: 128 bytes a lane
 
@@ -84,11 +55,15 @@ template <int G, int RT> struct Block {
   float s[RT][2];  // of group t of the block (t < P), shared in the quad
 };
 
-// One piece: 8 values of x (col, col + 8) of one token, by one of the 16 neighbouring threads of a block and token
-// (c = 0..15, all 16 take part).  Stores the piece, and by one thread each the group's sum and the block's factor.
+// One piece: 8 values of x by one of the 16 neighbouring threads of a block and token (c = 0..15, all 16 take part):
+// the values in their frame and order, the group's sum as stored, the block's factor, and whether all is finite.
+struct PieceOfX {
+  uint4 h;
+  float sum, factor;
+  bool odd;
+};
 template <int G>
-__device__ __forceinline__ bool make_piece(uint4 v, bool bf16, int c, bool live, uint4* xf, float* sums, int ld) {
-  constexpr int P = Lanes<G>::P, WP = 4 / P;
+__device__ __forceinline__ PieceOfX make_piece(uint4 v, bool bf16) {
   const uint32_t e[4] = {v.x, v.y, v.z, v.w};
   float f[8], top = 0.f;
 #pragma unroll
@@ -102,19 +77,18 @@ __device__ __forceinline__ bool make_piece(uint4 v, bool bf16, int c, bool live,
   for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const int fe = x_frame_exp(top);
   const float mul = exp2i(-fe), low = mul * 0.0625f;
+  PieceOfX r;
   // (k0,k4) (k1,k5)/16 (k2,k6) (k3,k7)/16
-  const uint4 h = make_uint4(pack_half2(f[0] * mul, f[4] * mul), pack_half2(f[1] * low, f[5] * low),
-                             pack_half2(f[2] * mul, f[6] * mul), pack_half2(f[3] * low, f[7] * low));
-  const float2 s0 = Elem<__half>::unpack(h.x), s1 = Elem<__half>::unpack(h.y), s2 = Elem<__half>::unpack(h.z), s3 = Elem<__half>::unpack(h.w);
+  r.h = make_uint4(pack_half2(f[0] * mul, f[4] * mul), pack_half2(f[1] * low, f[5] * low),
+                   pack_half2(f[2] * mul, f[6] * mul), pack_half2(f[3] * low, f[7] * low));
+  const float2 s0 = Elem<__half>::unpack(r.h.x), s1 = Elem<__half>::unpack(r.h.y), s2 = Elem<__half>::unpack(r.h.z), s3 = Elem<__half>::unpack(r.h.w);
   float sum = (s0.x + s0.y) + (s2.x + s2.y) + 16.f * ((s1.x + s1.y) + (s3.x + s3.y));
 #pragma unroll
   for (int o = 1; o < G / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (!live) return false;
-  const int p = c / (G / 8), cp = c % (G / 8), ct = cp / (G / 32), j = p * WP + cp % (G / 32);
-  xf[j * 32 + ct] = h;  // xf: of the block, token tile and token row
-  if (cp == 0) sums[p * ld] = sum * (-8.f * 0x1p-24f);
-  if (c == 0) sums[P * ld] = exp2i(fe + 12);
-  return !(fabsf(sum) < INFINITY);
+  r.sum = sum * (-8.f * 0x1p-24f);
+  r.factor = exp2i(fe + 12);
+  r.odd = !(fabsf(sum) < INFINITY);
+  return r;
 }
 
 // The weight stream of a warp: its blocks of every tile of the CTA, in order.
@@ -349,7 +323,14 @@ __global__ void __launch_bounds__(NW * 32, 1) linear_int4_kernel(LinearArgs a) {
     for (int k = 0; k < B; ++k) {
       const int i = w0 + lane + k * NW * 32, bm = i >> 4, b = bm / a.M, m = bm - b * a.M;
       if (w0 + k * NW * 32 >= pieces) break;
-      if (make_piece<G>(v[k], a.bf16, i & 15, i < pieces, xf + b * 128 + m * 4, sums + b * (P + 1) * 8 + m, 8)) odd = 1;
+      const PieceOfX x = make_piece<G>(v[k], a.bf16);
+      if (i < pieces) {
+        const int c = i & 15, p = c / (G / 8), cp = c % (G / 8);
+        xf[b * 128 + (p * (4 / P) + cp % (G / 32)) * 32 + m * 4 + cp / (G / 32)] = x.h;
+        if (cp == 0) sums[(b * (P + 1) + p) * 8 + m] = x.sum;
+        if (c == 0) sums[(b * (P + 1) + P) * 8 + m] = x.factor;
+        if (x.odd) odd = 1;
+      }
     }
   }
   __syncthreads();
@@ -389,102 +370,18 @@ __global__ void __launch_bounds__(256) linear_pieces_kernel(LinearArgs a) {
     const int m = m0 + (threadIdx.x >> 4);
     uint4 v = make_uint4(0, 0, 0, 0);
     if (m < a.M && col < a.K) v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ldx + col);
-    odd |= make_piece<G>(v, a.bf16, c, m < a.M, a.xf + (static_cast<long long>(b) * a.nt + (m >> 3)) * 128 + (m & 7) * 4,
-                         a.sums + static_cast<long long>(b) * (P + 1) * a.nt * 8 + m, a.nt * 8);
+    const PieceOfX x = make_piece<G>(v, a.bf16);
+    if (m < a.M) {
+      float* sums = a.sums + static_cast<long long>(b) * (P + 1) * a.tokens + m;
+      a.xf[static_cast<long long>(m) * gridDim.x * 16 + b * 16 + c] = x.h;
+      if (c % (G / 8) == 0) sums[c / (G / 8) * a.tokens] = x.sum;
+      if (c == 0) sums[P * a.tokens] = x.factor;
+      odd |= x.odd;
+    }
   }
   odd = __syncthreads_or(odd);
   if (threadIdx.x < 4) a.odd[b * 4 + threadIdx.x] = odd ? 1.f : 0.f;
-}
-
-// Any M and K, x from the workspace: NT tiles of 8 tokens a CTA, a ring of R steps (quarters of a block) a warp.
-template <int G, int NT, int NW> struct WideCfg {
-  static constexpr int R = NT == 8 ? 4 : 8;
-  static constexpr int kSums = (Lanes<G>::P + 1) * NT * 32 + 16;        // bytes of a block's sums, factors and mark
-  static constexpr int kWarp = R * NT * 512 + 4 * kSums;                // ring, then the sums of four blocks
-  static constexpr size_t kSmem = static_cast<size_t>(NW) * (kWarp + (NT < 4 ? NT : 4) * 8 * 36 * 4);
-  static_assert(kSmem <= kLinearSmem, "shared memory");
-};
-
-template <int G, int NT, int NW>
-__global__ void __launch_bounds__(NW * 32, 1) linear_int4_wide_kernel(LinearArgs a) {
-  using W = WideCfg<G, NT, NW>;
-  constexpr int P = Lanes<G>::P, RT = 2, U = kInFlight<RT>, R = W::R;
-  extern __shared__ __align__(16) unsigned char smem[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = lane & 3;
-  unsigned char* ring = smem + warp * W::kWarp;
-  float* red = reinterpret_cast<float*>(smem + NW * W::kWarp);
-  const int nt0 = blockIdx.y * NT, m0 = nt0 * 8, live_m = min(NT * 8, a.M - m0);
-  pdl_trigger();
-  pdl_wait();
-  Stream<G, RT, NW> st(a, warp, lane);
-  Block<G, RT> buf[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) st.fetch(buf[u], t);
-
-  // the stream of x: the steps of the same blocks, R steps ahead; token tiles past the last one repeat it
-  int x_tile = blockIdx.x, x_it = 0, x_blk = st.start(0), x_round = 0, x_sums = 0;
-  auto issue = [&](int j, int slot) {  // step j of the next block
-    if (x_tile < st.tiles && x_blk < st.nblk) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const long long at = (static_cast<long long>(x_blk) * a.nt + min(nt0 + n, a.nt - 1)) * 4 + j;
-        cp_async16_ca(ring + (slot * NT + n) * 512 + lane * 16, a.xf + at * 32 + lane);
-      }
-      if (j == 0)
-        for (int i = lane; i <= (P + 1) * NT * 2; i += 32) {
-          const int p = i / (NT * 2), q = i % (NT * 2), tl = min(nt0 + (q >> 1), a.nt - 1);
-          const float* src = p > P ? a.odd + x_blk * 4
-                                   : a.sums + (static_cast<long long>(x_blk) * (P + 1) + p) * a.nt * 8 + tl * 8 + (q & 1) * 4;
-          cp_async16_ca(ring + R * NT * 512 + x_sums * W::kSums + i * 16, src);
-        }
-    }
-    cp_commit();
-    if (j == 3) {
-      x_sums = (x_sums + 1) & 3;
-      x_blk += st.wk;
-      if (++x_round == st.rounds) { x_round = 0; x_tile += gridDim.x; x_blk = st.start(++x_it); }
-    }
-  };
-#pragma unroll
-  for (int i = 0; i < R; ++i) issue(i & 3, i);
-  int c_sums = 0;
-  for (int it = 0, tile = blockIdx.x; tile < st.tiles; ++it, tile += gridDim.x) {
-    float acc[RT][NT][4];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.f;
-    int blk = st.start(it);
-    for (int rd = 0; rd < st.rounds; rd += U)
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int s0 = R == 8 ? u * 4 : 0;  // the block's first slot
-        if (blk < st.nblk) {
-          const float* sums = reinterpret_cast<const float*>(ring + R * NT * 512 + c_sums * W::kSums);
-          cp_wait<R - 1>();  // the block's first step, its sums and mark
-          __syncwarp();      // which other lanes fetched; the pieces of a lane are its own
-          auto piece = [&](int n, int j) {
-            if (n == 0 && j > 0) cp_wait<R - 1>();
-            const uint4 v = *reinterpret_cast<const uint4*>(ring + ((s0 + j) * NT + n) * 512 + lane * 16);
-            if (n == NT - 1) issue(j, s0 + j);
-            return v;
-          };
-          if (sums[(P + 1) * NT * 8] == 0.f) multiply<G, NT, RT, true>(buf[u], acc, sums, NT * 8, t, piece);
-          else multiply<G, NT, RT, false>(buf[u], acc, sums, NT * 8, t, piece);
-          __syncwarp();      // all have read the sums
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) issue(j, s0 + j);
-        }
-        c_sums = (c_sums + 1) & 3;
-        blk += st.wk;
-        st.fetch(buf[u], t);
-      }
-    join_and_write<NT, RT, NW>(a, acc, red, tile, st.wk, st.gated, m0, live_m);
-  }
-  cp_wait<0>();
+  if (b == 0 && threadIdx.x == 0) *a.status = DeviceStatus{};
 }
 
 // Blocks of K that a CTA of the one-launch kernel can hold.
@@ -516,60 +413,60 @@ cudaError_t launch_resident(LinearArgs a, int sms, cudaStream_t s) {
   return launch_kernel(kern, dim3(tiles < sms ? tiles : sms), dim3(NW * 32), smem, s, true, a);
 }
 
-template <int G, int NT, int NW>
-cudaError_t launch_wide(LinearArgs a, int sms, cudaStream_t s) {
-  const int RW = a.gated ? 16 : 32, nblk = (a.K + kKBlock - 1) / kKBlock;
-  cudaError_t err = launch_kernel(linear_pieces_kernel<G>, dim3(nblk), dim3(256), 0, s, true, a);
-  if (err != cudaSuccess) return err;
-  a.wr = choose_wr(a, RW, NW, sms);
-  const int tiles = (a.N + RW * a.wr - 1) / (RW * a.wr);
-  auto kern = linear_int4_wide_kernel<G, NT, NW>;
-  constexpr int smem = static_cast<int>(WideCfg<G, NT, NW>::kSmem);
-  err = set_smem_limit_once(reinterpret_cast<const void*>(kern), smem);
-  if (err != cudaSuccess) return err;
-  return launch_kernel(kern, dim3(tiles < sms ? tiles : sms, (a.nt + NT - 1) / NT), dim3(NW * 32), smem, s, true, a);
-}
-
 template <int G>
-cudaError_t launch_linear(const LinearArgs& a, int sms, cudaStream_t s) {
-  if (!a.xf) {
+cudaError_t launch_linear(const LinearArgs& a, const WidePlan* wide, int sms, cudaStream_t s) {
+  if (!wide) {
     // 16 or 32 rows a warp: whichever leaves the busiest SM with fewer rows
     const int t1 = (a.N + 15) / 16, t2 = (a.N + 31) / 32;
     const int r1 = (t1 + sms - 1) / sms * 16, r2 = (t2 + sms - 1) / sms * 32;
     return !a.gated && r1 < r2 ? launch_resident<G, 1>(a, sms, s) : launch_resident<G, 2>(a, sms, s);
   }
-  if (a.nt == 1) return launch_wide<G, 1, 16>(a, sms, s);
-  if (a.nt == 2) return launch_wide<G, 2, 16>(a, sms, s);
-  if (a.nt <= 4) return launch_wide<G, 4, 8>(a, sms, s);
-  return launch_wide<G, 8, 8>(a, sms, s);
+  cudaError_t err = launch_kernel(linear_pieces_kernel<G>, dim3((a.K + kKBlock - 1) / kKBlock), dim3(256), 0, s, true, a);
+  return err != cudaSuccess ? err : launch_wide_tc(a, G, *wide, s);
 }
 
-struct LinearLayout { size_t sums = 0, odd = 0, total = 0; };  // the pieces stand first
-bool linear_layout(int M, int K, int group, LinearLayout* l) {  // false: no workspace is needed
-  const int nblk = (K + kKBlock - 1) / kKBlock;
+bool needs_workspace(int M, int K, int group) {
   const int fit = group == 128 ? kResidentBlocks<128> : group == 64 ? kResidentBlocks<64> : kResidentBlocks<32>;
-  if (M <= 8 && nblk <= fit) return false;
-  const size_t nt = (static_cast<size_t>(M) + 7) / 8;
-  l->sums = nblk * nt * 2048;
-  l->odd = l->sums + nblk * nt * 32 * (128 / group + 1);
-  l->total = l->odd + static_cast<size_t>(nblk) * 16;
-  return true;
+  return M > 8 || (K + kKBlock - 1) / kKBlock > fit;
+}
+
+struct LinearLayout { size_t x = 0, sums = 0, odd = 0, part = 0, total = 0; };  // the status words stand first
+LinearLayout linear_layout(int K, int group, const WidePlan& p) {
+  LinearLayout l;
+  const size_t nblk = (static_cast<size_t>(K) + kKBlock - 1) / kKBlock, tokens = static_cast<size_t>(p.parts) * p.mt;
+  size_t at = kStatusBytes;
+  auto take = [&](size_t n) { const size_t r = at; at = (at + n + 255) / 256 * 256; return r; };
+  l.x = take(tokens * nblk * 256);
+  l.sums = take(nblk * tokens * 4 * (128 / group + 1));
+  l.odd = take(nblk * 16);
+  l.part = take(p.part_bytes);
+  l.total = at;
+  return l;
+}
+
+bool valid_sizes(int M, int N, int K) {
+  return M <= (1 << 19) && N <= (1 << 29) && K <= (1 << 25);  // (65,535 parts of 16 tokens at most)
 }
 
 }  // namespace
+}  // namespace linear
 }  // namespace gbmoe
 
-extern "C" size_t moe_linear_int4_workspace_size(int M, int K, int group) {
+extern "C" size_t moe_linear_int4_workspace_size(int M, int N, int K, int group, int gated) {
   using namespace gbmoe;
-  LinearLayout l;
-  if (M <= 0 || M > (1 << 20) || K <= 0 || K > (1 << 25) || (group != 32 && group != 64 && group != 128) || K % group) return 0;
-  return linear_layout(M, K, group, &l) ? l.total : 0;
+  using namespace gbmoe::linear;
+  if (M <= 0 || N <= 0 || K <= 0 || !valid_sizes(M, N, K) || (group != 32 && group != 64 && group != 128) || K % group ||
+      !needs_workspace(M, K, group))
+    return 0;
+  const int sms = num_sms_current();
+  return linear_layout(K, group, wide_plan(M, N, K, group, gated != 0, sms > 0 ? sms : kMaxSms)).total;
 }
 
 extern "C" moe_status_t moe_linear_int4(int dtype, const void* x, int64_t x_stride, const uint8_t* w, const float* w_scale,
                                         int M, int N, int K, int group, int gated, void* y, int64_t y_stride,
                                         void* workspace, size_t workspace_bytes, moe_stream_t stream) {
   using namespace gbmoe;
+  using namespace gbmoe::linear;
   return guarded("moe_linear_int4", [&]() -> moe_status_t {
     auto bad = [](const char* m) { return report_error(MOE_ERR_INVALID_ARG, std::string("moe_linear_int4: ") + m); };
     if (dtype != MOE_DTYPE_BF16 && dtype != MOE_DTYPE_FP16) return bad("x must be bf16 or fp16");
@@ -578,7 +475,7 @@ extern "C" moe_status_t moe_linear_int4(int dtype, const void* x, int64_t x_stri
       return report_error(MOE_ERR_UNSUPPORTED, "moe_linear_int4: the group size must be 32, 64 or 128");
     if (K % group) return bad("K must be a multiple of the group size");
     if (gated != 0 && gated != 1) return bad("gated must be 0 or 1");
-    if (M > (1 << 20) || N > (1 << 29) || K > (1 << 25))
+    if (!valid_sizes(M, N, K))
       return report_error(MOE_ERR_UNSUPPORTED, "moe_linear_int4: problem too large");
     if (M == 0) return MOE_OK;
     if (!x || !w || !w_scale || !y) return bad("NULL pointer");
@@ -587,18 +484,28 @@ extern "C" moe_status_t moe_linear_int4(int dtype, const void* x, int64_t x_stri
     if (!aligned(w_scale, 4) || !aligned(y, 2)) return bad("unaligned scales or output");
     const int sms = num_sms_current();
     if (sms <= 0) return report_error(MOE_ERR_CUDA, "moe_linear_int4: no CUDA device");
-    LinearArgs a{x, w, w_scale, y, x_stride, y_stride, M, N, K, gated, dtype == MOE_DTYPE_BF16, 1, (M + 7) / 8, nullptr, nullptr, nullptr};
-    LinearLayout l;
-    if (linear_layout(M, K, group, &l)) {
+    LinearArgs a{};
+    a.x = x; a.w = w; a.scale = w_scale; a.y = y;
+    a.ldx = x_stride; a.ldy = y_stride;
+    a.M = M; a.N = N; a.K = K; a.gated = gated; a.bf16 = dtype == MOE_DTYPE_BF16;
+    WidePlan p;
+    const bool wide = needs_workspace(M, K, group);
+    if (wide) {
+      p = wide_plan(M, N, K, group, gated, sms);
+      const LinearLayout l = linear_layout(K, group, p);
       if (!workspace || workspace_bytes < l.total || !aligned(workspace, 256))
         return report_error(MOE_ERR_WORKSPACE, "moe_linear_int4: workspace NULL, misaligned or too small");
       char* ws = static_cast<char*>(workspace);
-      a.xf = reinterpret_cast<uint4*>(ws);
+      a.tokens = p.parts * p.mt;
+      a.status = reinterpret_cast<DeviceStatus*>(ws);
+      a.xf = reinterpret_cast<uint4*>(ws + l.x);
       a.sums = reinterpret_cast<float*>(ws + l.sums);
       a.odd = reinterpret_cast<float*>(ws + l.odd);
+      a.part = reinterpret_cast<float*>(ws + l.part);
     }
+    const WidePlan* wp = wide ? &p : nullptr;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return launched("moe_linear_int4", group == 128 ? launch_linear<128>(a, sms, s)
-                                       : group == 64 ? launch_linear<64>(a, sms, s) : launch_linear<32>(a, sms, s));
+    return launched("moe_linear_int4", group == 128 ? launch_linear<128>(a, wp, sms, s)
+                                       : group == 64 ? launch_linear<64>(a, wp, sms, s) : launch_linear<32>(a, wp, sms, s));
   });
 }

@@ -77,7 +77,7 @@ _SIGS = {
     "moe_profile_enable": (_i, [_i]),
     "moe_profile_read": (_i, [_vp, _vp, _i, _vp, _vp]),
     "moe_rope": (_i, [_vp, _vp]),
-    "moe_linear_int4_workspace_size": (_sz, [_i] * 3),
+    "moe_linear_int4_workspace_size": (_sz, [_i] * 5),
     "moe_linear_int4": (_i, [_i, _vp, _i64, _vp, _vp] + [_i] * 5 + [_vp, _i64, _vp, _sz, _vp]),
     "moe_tree_attention_workspace_size": (_sz, [_i] * 5),
     "moe_tree_attention": (_i, [_vp, _vp, _sz, _vp]),
@@ -599,8 +599,8 @@ def moe_rope_append(q, k, v, positions, inv_freq, slots, k_cache, v_cache, scale
     return q_out
 
 
-def moe_linear_int4_workspace_size(M, K, group) -> int:
-    return int(load().moe_linear_int4_workspace_size(M, K, group))
+def moe_linear_int4_workspace_size(M, N, K, group, gated=False) -> int:
+    return int(load().moe_linear_int4_workspace_size(M, N, K, group, 1 if gated else 0))
 
 
 def moe_linear_int4(x, w, w_scale, gated=False, out=None, workspace=None):
@@ -625,7 +625,7 @@ def moe_linear_int4(x, w, w_scale, gated=False, out=None, workspace=None):
         raise ValueError("out must be [M, N] of x's type with contiguous rows")
     lib, group, ws, ws_bytes = load(), K // groups, 0, 0
     if workspace is None and (M > 8 or K > 8192):
-        n = lib.moe_linear_int4_workspace_size(M, K, group)
+        n = lib.moe_linear_int4_workspace_size(M, N, K, group, 1 if gated else 0)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
     if workspace is not None:
