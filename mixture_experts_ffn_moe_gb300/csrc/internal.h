@@ -214,6 +214,9 @@ cudaError_t launch_combine(const __nv_bfloat16* y, const int32_t* inv_pos, int M
 // 2D row-major tensor [outer, inner] of `esize`-byte elements, TMA box [box_outer, box_inner].
 bool encode_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, int esize, const void* base, uint64_t inner,
                     uint64_t outer, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
+// 16-bit elements [rows, halves, 64]: boxes of two neighbouring halves of box_rows rows, each half a 128-byte-swizzled
+// tile of its own.
+bool encode_tmap_halves(CUtensorMap* m, const void* base, int halves, int rows, int box_rows);
 // A paged cache of 16-bit elements as a tensor [pages, heads, page_size, dim] (strides in elements), 128-byte-swizzled
 // boxes of box_slots rows of one page and head.  False where the strides do not fit a tensor map.
 bool encode_tmap_cache(CUtensorMap* m, const void* base, int dim, int page_size, int heads, int pages, long long slot,

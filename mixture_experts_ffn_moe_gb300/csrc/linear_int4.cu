@@ -358,30 +358,28 @@ __global__ void __launch_bounds__(NW * 32, 1) linear_int4_kernel(LinearArgs a) {
   }
 }
 
-// x into the workspace: one CTA a block of K, 16 threads a token.
+// x into the workspace: a CTA a block of K and 16 tokens, 16 threads a token.
 template <int G>
 __global__ void __launch_bounds__(256) linear_pieces_kernel(LinearArgs a) {
   constexpr int P = Lanes<G>::P;
   pdl_trigger();
   pdl_wait();
-  const int b = blockIdx.x, c = threadIdx.x & 15, col = b * kKBlock + c * 8;
-  bool odd = false;
-  for (int m0 = 0; m0 < a.M; m0 += 16) {
-    const int m = m0 + (threadIdx.x >> 4);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (m < a.M && col < a.K) v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ldx + col);
-    const PieceOfX x = make_piece<G>(v, a.bf16);
-    if (m < a.M) {
-      float* sums = a.sums + static_cast<long long>(b) * (P + 1) * a.tokens + m;
-      a.xf[static_cast<long long>(m) * gridDim.x * 16 + b * 16 + c] = x.h;
-      if (c % (G / 8) == 0) sums[c / (G / 8) * a.tokens] = x.sum;
-      if (c == 0) sums[P * a.tokens] = x.factor;
-      odd |= x.odd;
-    }
+  const int b = blockIdx.x, c = threadIdx.x & 15, col = b * kKBlock + c * 8, m = blockIdx.y * 16 + (threadIdx.x >> 4);
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (m < a.M && col < a.K) v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ldx + col);
+  const PieceOfX x = make_piece<G>(v, a.bf16);
+  const int part = m / a.mt, mp = m - part * a.mt;
+  float* sums = a.sums + (static_cast<long long>(b) * (a.tokens / a.mt) + part) * ((P + 1) * a.mt + 4);
+  if (m < a.M) {
+    a.xf[static_cast<long long>(m) * gridDim.x * 16 + b * 16 + c] = x.h;
+    if (c % (G / 8) == 0) sums[c / (G / 8) * a.mt + mp] = x.sum;
+    if (c == 0) sums[P * a.mt + mp] = x.factor;
   }
-  odd = __syncthreads_or(odd);
-  if (threadIdx.x < 4) a.odd[b * 4 + threadIdx.x] = odd ? 1.f : 0.f;
-  if (b == 0 && threadIdx.x == 0) *a.status = DeviceStatus{};
+  const bool odd = __syncthreads_or(x.odd && m < a.M);
+  if (threadIdx.x == 0) {
+    sums[(P + 1) * a.mt + mp / 16] = odd ? 1.f : 0.f;
+    if (b == 0 && blockIdx.y == 0) *a.status = DeviceStatus{};
+  }
 }
 
 // Blocks of K that a CTA of the one-launch kernel can hold.
@@ -421,7 +419,7 @@ cudaError_t launch_linear(const LinearArgs& a, const WidePlan* wide, int sms, cu
     const int r1 = (t1 + sms - 1) / sms * 16, r2 = (t2 + sms - 1) / sms * 32;
     return !a.gated && r1 < r2 ? launch_resident<G, 1>(a, sms, s) : launch_resident<G, 2>(a, sms, s);
   }
-  cudaError_t err = launch_kernel(linear_pieces_kernel<G>, dim3((a.K + kKBlock - 1) / kKBlock), dim3(256), 0, s, true, a);
+  cudaError_t err = launch_kernel(linear_pieces_kernel<G>, dim3((a.K + kKBlock - 1) / kKBlock, a.tokens / 16), dim3(256), 0, s, true, a);
   return err != cudaSuccess ? err : launch_wide_tc(a, G, *wide, s);
 }
 
@@ -430,15 +428,14 @@ bool needs_workspace(int M, int K, int group) {
   return M > 8 || (K + kKBlock - 1) / kKBlock > fit;
 }
 
-struct LinearLayout { size_t x = 0, sums = 0, odd = 0, part = 0, total = 0; };  // the status words stand first
+struct LinearLayout { size_t x = 0, sums = 0, part = 0, total = 0; };  // the status words stand first
 LinearLayout linear_layout(int K, int group, const WidePlan& p) {
   LinearLayout l;
   const size_t nblk = (static_cast<size_t>(K) + kKBlock - 1) / kKBlock, tokens = static_cast<size_t>(p.parts) * p.mt;
   size_t at = kStatusBytes;
   auto take = [&](size_t n) { const size_t r = at; at = (at + n + 255) / 256 * 256; return r; };
   l.x = take(tokens * nblk * 256);
-  l.sums = take(nblk * tokens * 4 * (128 / group + 1));
-  l.odd = take(nblk * 16);
+  l.sums = take(nblk * p.parts * 4 * ((128 / group + 1) * static_cast<size_t>(p.mt) + 4));
   l.part = take(p.part_bytes);
   l.total = at;
   return l;
@@ -497,10 +494,10 @@ extern "C" moe_status_t moe_linear_int4(int dtype, const void* x, int64_t x_stri
         return report_error(MOE_ERR_WORKSPACE, "moe_linear_int4: workspace NULL, misaligned or too small");
       char* ws = static_cast<char*>(workspace);
       a.tokens = p.parts * p.mt;
+      a.mt = p.mt;
       a.status = reinterpret_cast<DeviceStatus*>(ws);
       a.xf = reinterpret_cast<uint4*>(ws + l.x);
       a.sums = reinterpret_cast<float*>(ws + l.sums);
-      a.odd = reinterpret_cast<float*>(ws + l.odd);
       a.part = reinterpret_cast<float*>(ws + l.part);
     }
     const WidePlan* wp = wide ? &p : nullptr;

@@ -17,8 +17,9 @@ struct LinearArgs {
   // more than 8 rows (workspace): x as the products take it
   int tokens;          // M rounded up to whole products
   uint4* xf;           // fp16 [tokens][blocks * 128], each 8 columns in the codes' order
-  float* sums;         // [blocks][P + 1][tokens]: -8 * 2^-24 * the groups' sums, then 2^(frame + 12)
-  float* odd;          // [blocks][4] not 0 where a block holds infinities or NaN
+  int mt;              // tokens of a product
+  float* sums;         // [blocks][tokens / mt][(P + 1) * mt + 4]: -8 * 2^-24 * the groups' sums, 2^(frame + 12), and
+                       // for every 16 tokens a mark that is not 0 where they hold infinities or NaN
   float* part;         // fp32 parts of cut tiles
   DeviceStatus* status;
   long long chunk;     // blocks a CTA

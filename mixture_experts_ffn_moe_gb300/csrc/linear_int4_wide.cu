@@ -154,7 +154,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(fine = warp_wait(&sm.full[st], (n / NS) & 1))) break;
         const unsigned char* stage = base + st * C::kStage;
         const float* sums = reinterpret_cast<const float*>(stage + kCodeBytes + C::kX);
-        const bool odd = sums[(P + 1) * MT] != 0.f;
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < MT / 16; ++i) odd |= i * 16 < live_m && sums[(P + 1) * MT + i] != 0.f;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {  // 16 bytes, 32 codes, 16 columns of U
           const uint4 v = *reinterpret_cast<const uint4*>(stage + row * 64 + ((c ^ ((row >> 1) & 3)) << 4));
@@ -245,32 +247,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kGroupsOfWarps * 4) {
     // ---------------------------------------------------------------- loads
-    if (lane == 0) {
+    {
       int n = 0;
       bool fine = true;
       int tile = static_cast<int>(first / nblk), b = static_cast<int>(first - static_cast<long long>(tile) * nblk);
       for (long long pos = first; pos < end; ++pos, ++n) {
         const int st = n % NS;
-        if (!(fine = wait(&sm.empty[st], ((n / NS) & 1) ^ 1))) break;
+        if (!(fine = __all_sync(0xffffffffu, wait(&sm.empty[st], ((n / NS) & 1) ^ 1)) != 0)) break;
         unsigned char* stage = base + st * C::kStage;
-        mbar_arrive_expect_tx(&sm.full[st], kCodeBytes + C::kX + C::kSums);
-        if (a.gated) {
-          tma_load_2d(stage, &mw, &sm.full[st], b * 64, tile * 64);
-          tma_load_2d(stage + 64 * 64, &mw, &sm.full[st], b * 64, a.N + tile * 64);
-        } else {
-          tma_load_2d(stage, &mw, &sm.full[st], b * 64, tile * 128);
-          tma_load_2d(stage + 64 * 64, &mw, &sm.full[st], b * 64, tile * 128 + 64);
+        if (lane == 0) mbar_arrive_expect_tx(&sm.full[st], kCodeBytes + C::kX + C::kSums);
+        __syncwarp();
+        if (lane < 2) {  // 64 rows each
+          const int row = a.gated ? lane * a.N + tile * 64 : tile * 128 + lane * 64;
+          tma_load_2d(stage + lane * 64 * 64, &mw, &sm.full[st], b * 64, row);
+        } else if (lane == 2) {
+          tma_load_3d(smem_addr(stage + kCodeBytes), &mx, &sm.full[st], 0, m0, b * 2);
+        } else if (lane == 3) {
+          bulk_load(smem_addr(stage + kCodeBytes + C::kX),
+                    a.sums + (static_cast<long long>(b) * gridDim.y + blockIdx.y) * ((P + 1) * MT + 4), C::kSums, &sm.full[st]);
         }
-        tma_load_2d(stage + kCodeBytes, &mx, &sm.full[st], b * 128, m0);
-        tma_load_2d(stage + kCodeBytes + C::kX / 2, &mx, &sm.full[st], b * 128 + 64, m0);
-        const uint32_t sums = smem_addr(stage + kCodeBytes + C::kX);
-#pragma unroll
-        for (int p = 0; p <= P; ++p)
-          bulk_load(sums + p * MT * 4, a.sums + (static_cast<long long>(b) * (P + 1) + p) * a.tokens + m0, MT * 4, &sm.full[st]);
-        bulk_load(sums + (P + 1) * MT * 4, a.odd + static_cast<long long>(b) * 4, 16, &sm.full[st]);
         if (++b == nblk) { b = 0; ++tile; }
       }
-      if (!fine) {  // copies on their way land before the CTA goes
+      if (!fine && lane == 0) {  // copies on their way land before the CTA goes
         int none = 0;
         for (int t = max(0, n - NS); t < n; ++t) mbar_wait(&sm.full[t % NS], (t / NS) & 1, &none, nullptr, kLimit);
       }
@@ -310,30 +308,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Adds up the parts of the tiles that were cut: a CTA a tile and 64 of its rows (gated: 32 gate rows with their up rows).
+// Adds up the parts of the tiles that were cut, in order: four neighbouring rows of a token a thread.
 template <int MT>
-__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ LinearArgs a, int ctas) {
+__global__ void __launch_bounds__(128) linear_join_kernel(const __grid_constant__ LinearArgs a, int ctas) {
   pdl_trigger();
   pdl_wait();
   const int nblk = (a.K + 127) / 128, tile = blockIdx.x, m0 = blockIdx.y * MT, live_m = min(MT, a.M - m0);
   const long long s = static_cast<long long>(tile) * nblk, e = s + nblk;
-  const long long c0 = s / a.chunk, c1 = (e - 1) / a.chunk;
+  const int c0 = static_cast<int>(s / a.chunk), c1 = static_cast<int>((e - 1) / a.chunk);
   if (c0 == c1) return;
-  const int rows = a.gated ? 64 : 128;
-  auto sum = [&](int row, int m) {
-    float v = 0.f;
+  const int quads = a.gated ? 16 : 32, i = blockIdx.z * 128 + threadIdx.x;
+  const int row = i % quads * 4, m = i / quads;
+  if (m >= live_m) return;
+  auto sum = [&](int r) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (long long c = c0; c <= c1; ++c) {
-      const long long slot = (static_cast<long long>(blockIdx.y) * ctas + c) * 2 + (c * a.chunk > s ? 0 : 1);
-      v += a.part[slot * (kRows * MT) + m * kRows + row];
+    for (int c = c0; c <= c1; ++c) {
+      const long long slot = (static_cast<long long>(blockIdx.y) * ctas + c) * 2 + (c > c0 ? 0 : 1);
+      const float4 p = *reinterpret_cast<const float4*>(a.part + slot * (kRows * MT) + m * kRows + r);
+      v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
     }
-    return v * 4096.f;
+    return v;
   };
-  for (int i = threadIdx.x + blockIdx.z * 256; i < rows * live_m; i += 256 * gridDim.z) {
-    const int row = i % rows, m = i / rows, n = tile * rows + row;
-    if (n >= a.N) continue;
-    const float v = sum(row, m);
-    store(a, m0 + m, n, a.gated ? silu_f32(v) * sum(row + 64, m) : v);
+  const float4 v = sum(row);
+  const float y[4] = {v.x * 4096.f, v.y * 4096.f, v.z * 4096.f, v.w * 4096.f};
+  float up[4] = {};
+  if (a.gated) {
+    const float4 u = sum(row + 64);
+    up[0] = u.x * 4096.f; up[1] = u.y * 4096.f; up[2] = u.z * 4096.f; up[3] = u.w * 4096.f;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int n = tile * quads * 4 + row + j;
+    if (n < a.N) store(a, m0 + m, n, a.gated ? silu_f32(y[j]) * up[j] : y[j]);
   }
 }
 
@@ -344,8 +351,7 @@ cudaError_t launch(LinearArgs a, const WidePlan& p, cudaStream_t s) {
   const int nblk = (a.K + 127) / 128;
   if (!encode_tmap_2d(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.w, static_cast<uint64_t>(a.K) / 2, static_cast<uint64_t>(a.N) * (a.gated ? 2 : 1),
                       64, 64, CU_TENSOR_MAP_SWIZZLE_64B) ||
-      !encode_tmap_2d(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, a.xf, static_cast<uint64_t>(nblk) * 128, static_cast<uint64_t>(a.tokens), 64, MT,
-                      CU_TENSOR_MAP_SWIZZLE_128B))
+      !encode_tmap_halves(&mx, a.xf, nblk * 2, a.tokens, MT))
     return cudaErrorInvalidValue;
   a.chunk = p.chunk;
   auto kern = linear_tc_kernel<G, MT>;
@@ -354,8 +360,8 @@ cudaError_t launch(LinearArgs a, const WidePlan& p, cudaStream_t s) {
   err = launch_kernel(kern, dim3(p.ctas, p.parts), dim3(kThreads), C::kSmem, s, true, a, mw, mx);
   if (err != cudaSuccess || !p.cut) return err;
   const int tiles = (a.N + (a.gated ? 63 : 127)) / (a.gated ? 64 : 128);
-  const int z = tiles * p.parts < 152 ? 4 : 1;
-  return launch_kernel(linear_join_kernel<MT>, dim3(tiles, p.parts, z), dim3(256), 0, s, true, a, p.ctas);
+  const int z = (a.M < MT ? a.M : MT) * (a.gated ? 16 : 32);
+  return launch_kernel(linear_join_kernel<MT>, dim3(tiles, p.parts, (z + 127) / 128), dim3(128), 0, s, true, a, p.ctas);
 }
 
 }  // namespace

@@ -708,6 +708,18 @@ bool encode_tmap_2d(CUtensorMap* m, CUtensorMapDataType dt, int esize, const voi
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_tmap_halves(CUtensorMap* m, const void* base, int halves, int rows, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(halves)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(halves) * 128, 128};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 2};
+  const cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_tmap_cache(CUtensorMap* m, const void* base, int dim, int page_size, int heads, int pages, long long slot,
                        long long head, long long page, int box_dim, int box_slots) {
   EncodeTiledFn fn = encode_fn();

@@ -7,6 +7,7 @@ There is no fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import struct
@@ -448,37 +449,39 @@ _ROPE_ARGS = struct.Struct("@9if2i3P3P3P6q5q3q")
 _TREE_ARGS = struct.Struct("@9ifq3P3PPP4q6q")
 
 
-def _raw_stream(t: torch.Tensor) -> int:
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+# A decode step makes many short calls, so the bindings test their arguments in one expression and look for the
+# reason only where it fails.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _fail_tensor(t, device, dtype, shape, name, contiguous):
+    """Raises ValueError if `t` is not a CUDA tensor of this device, type and shape (None: any size)."""
+    if t.get_device() < 0 or t.get_device() != device:
+        raise ValueError(f"{name} must be a CUDA tensor on the device of the other tensors")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name} has the shape {list(t.shape)}, expected {['any' if w is None else w for w in shape]}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not contiguous and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def _fail(device, *checks):
+    """Raises the first error of (tensor, dtype, shape, name, contiguous) checks."""
+    for t, dtype, shape, name, contiguous in checks:
+        _fail_tensor(t, device, dtype, shape, name, contiguous)
+    raise ValueError("inconsistent arguments")
 
 
 def _float_dtype(t: torch.Tensor, name: str, allowed) -> int:
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
     d = _DTYPES.get(t.dtype)
     if d is None or d not in allowed:
         raise ValueError(f"{name} has an unsupported type {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
     return d
-
-
-def _rows3(t: torch.Tensor, dtype, name: str):
-    """(token stride, head stride) of a [tokens, heads, dim] tensor with a contiguous last dimension."""
-    if not t.is_cuda or t.dtype != dtype or t.dim() != 3:
-        raise ValueError(f"{name} must be a CUDA tensor [tokens, heads, dim] of type {dtype}")
-    st = t.stride()
-    if st[2] != 1 and t.shape[2] > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    return st
-
-
-def _pages4(t: torch.Tensor, dtype, name: str):
-    """Strides of a [pages, page_size, heads, dim] cache with a contiguous last dimension (any order of the rest)."""
-    if not t.is_cuda or t.dtype != dtype or t.dim() != 4:
-        raise ValueError(f"{name} must be a CUDA tensor [pages, page_size, heads, dim] of type {dtype}")
-    st = t.stride()
-    if st[3] != 1 and t.shape[3] > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    return st
 
 
 def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, original_positions=0, beta_fast=32.0,
@@ -518,15 +521,6 @@ def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, original
     return f.to(device), scale
 
 
-def _rope_tables(positions, inv_freq, tokens):
-    if not positions.is_cuda or positions.dtype != torch.int32 or not positions.is_contiguous():
-        raise ValueError("positions must be a contiguous int32 CUDA tensor")
-    if not inv_freq.is_cuda or inv_freq.dtype != torch.float64 or not inv_freq.is_contiguous():
-        raise ValueError("inv_freq must be a contiguous float64 CUDA tensor")
-    if positions.numel() != tokens:
-        raise ValueError("positions must have one entry a token")
-
-
 def moe_rope(q, k, positions, inv_freq, scale=1.0, interleaved=False, inverse=False, offset=0, q_out=None,
              k_out=None):
     """Rotary positions of q and k ([tokens, heads, dim], bf16 / fp16 / fp32; k may be None): (q_out, k_out).
@@ -534,31 +528,38 @@ def moe_rope(q, k, positions, inv_freq, scale=1.0, interleaved=False, inverse=Fa
     The 2 * len(inv_freq) elements from `offset` on turn by position * inv_freq; the rest is copied.  q_out and
     k_out may be the inputs (in place).  See include/gbmoe.h.
     """
+    dtype = q.dtype
     dt = _float_dtype(q, "q", (0, 1, 2))
-    qs = _rows3(q, q.dtype, "q")
+    dev = q.get_device()
+    if q.dim() != 3:
+        raise ValueError("q must be [tokens, heads, dim]")
     T, hq, D = q.shape
-    _rope_tables(positions, inv_freq, T)
     if q_out is None:
-        q_out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
-    elif q_out.shape != q.shape:
-        raise ValueError("q_out must have the shape of q")
-    qo = _rows3(q_out, q.dtype, "q_out")
-    hk, kp, kop, ks, ko = 0, 0, 0, (0, 0), (0, 0)
+        q_out = torch.empty((T, hq, D), dtype=dtype, device=q.device)
+    qt, qh, qd = q.stride()
+    ot, oh, od = q_out.stride()
+    if not ((qd == 1 or D == 1) and (od == 1 or D == 1) and q_out.dtype is dtype and q_out.get_device() == dev
+            and q_out.shape == q.shape and positions.dtype is torch.int32 and positions.get_device() == dev
+            and positions.shape == (T,) and positions.is_contiguous() and inv_freq.dtype is torch.float64
+            and inv_freq.get_device() == dev and inv_freq.dim() == 1 and inv_freq.is_contiguous()):
+        _fail(dev, (q, dtype, (T, hq, D), "q", False), (q_out, dtype, (T, hq, D), "q_out", False),
+              (positions, torch.int32, (T,), "positions", True), (inv_freq, torch.float64, (None,), "inv_freq", True))
+    hk = kp = kop = kt = kh = kot = koh = 0
     if k is not None:
-        ks = _rows3(k, q.dtype, "k")
-        hk = k.shape[1]
-        if k.shape[0] != T or k.shape[2] != D:
-            raise ValueError("q and k must have the same tokens and dim")
+        hk = k.shape[1] if k.dim() == 3 else 0
         if k_out is None:
-            k_out = torch.empty((T, hk, D), dtype=q.dtype, device=q.device)
-        elif k_out.shape != k.shape:
-            raise ValueError("k_out must have the shape of k")
-        ko = _rows3(k_out, q.dtype, "k_out")
+            k_out = torch.empty((T, hk, D), dtype=dtype, device=q.device)
+        if not (k.dtype is dtype and k_out.dtype is dtype and k.get_device() == dev and k_out.get_device() == dev
+                and k.shape == (T, hk, D) and k_out.shape == (T, hk, D)
+                and (D == 1 or (k.stride(2) == 1 and k_out.stride(2) == 1))):
+            _fail(dev, (k, dtype, (T, None, D), "k", False), (k_out, dtype, (T, hk, D), "k_out", False))
+        kt, kh, _ = k.stride()
+        kot, koh, _ = k_out.stride()
         kp, kop = k.data_ptr(), k_out.data_ptr()
-    args = _ROPE_ARGS.pack(dt, T, D, 2 * inv_freq.numel(), offset, interleaved, inverse, hq, hk, scale, 0, 0,
+    args = _ROPE_ARGS.pack(dt, T, D, 2 * inv_freq.shape[0], offset, interleaved, inverse, hq, hk, scale, 0, 0,
                            positions.data_ptr(), inv_freq.data_ptr(), 0, q.data_ptr(), kp, 0, q_out.data_ptr(), kop,
-                           0, qs[0], qs[1], ks[0], ks[1], 0, 0, qo[0], qo[1], 0, ko[0], ko[1], 0, 0, 0)
-    st = load().moe_rope(args, _raw_stream(q))
+                           0, qt, qh, kt, kh, 0, 0, ot, oh, 0, kot, koh, 0, 0, 0)
+    st = (_lib or load()).moe_rope(args, _raw_stream(dev))
     if st:
         _check(st, "moe_rope")
     return q_out, k_out
@@ -571,29 +572,42 @@ def moe_rope_append(q, k, v, positions, inv_freq, slots, k_cache, v_cache, scale
     slots int32 [tokens]: page * page_size + row in k_cache / v_cache [pages, page_size, k_heads, dim]; entries
     outside the cache (such as -1) are skipped.
     """
+    dtype = q.dtype
     dt = _float_dtype(q, "q", (0, 1, 2))
-    qs, ks, vs = _rows3(q, q.dtype, "q"), _rows3(k, q.dtype, "k"), _rows3(v, q.dtype, "v")
+    dev = q.get_device()
+    if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4:
+        raise ValueError("q and k must be [tokens, heads, dim], k_cache [pages, page_size, k_heads, dim]")
     T, hq, D = q.shape
     hk = k.shape[1]
-    _rope_tables(positions, inv_freq, T)
-    if k.shape[0] != T or k.shape[2] != D or v.shape != k.shape:
-        raise ValueError("q, k and v must have the same tokens and dim, k and v the same heads")
-    kc, vc = _pages4(k_cache, q.dtype, "k_cache"), _pages4(v_cache, q.dtype, "v_cache")
-    if k_cache.shape != v_cache.shape or k_cache.shape[2] != hk or k_cache.shape[3] != D:
-        raise ValueError("k_cache and v_cache must be [pages, page_size, k_heads, dim]")
-    if not slots.is_cuda or slots.dtype != torch.int32 or not slots.is_contiguous() or slots.numel() != T:
-        raise ValueError("slots must be a contiguous int32 CUDA tensor with one entry a token")
     if q_out is None:
-        q_out = torch.empty((T, hq, D), dtype=q.dtype, device=q.device)
-    elif q_out.shape != q.shape:
-        raise ValueError("q_out must have the shape of q")
-    qo = _rows3(q_out, q.dtype, "q_out")
-    args = _ROPE_ARGS.pack(dt, T, D, 2 * inv_freq.numel(), offset, interleaved, inverse, hq, hk, scale,
-                           k_cache.shape[1], k_cache.shape[0], positions.data_ptr(), inv_freq.data_ptr(),
-                           slots.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), q_out.data_ptr(),
-                           k_cache.data_ptr(), v_cache.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], qo[0],
-                           qo[1], kc[0], kc[1], kc[2], vc[0], vc[1], vc[2])
-    st = load().moe_rope(args, _raw_stream(q))
+        q_out = torch.empty((T, hq, D), dtype=dtype, device=q.device)
+    shape, cache = (T, hk, D), k_cache.shape
+    if not (k.shape == shape and v.shape == shape and q_out.shape == q.shape and cache == v_cache.shape
+            and cache[2] == hk and cache[3] == D and positions.shape == (T,) and slots.shape == (T,)
+            and k.dtype is dtype and v.dtype is dtype and q_out.dtype is dtype and k_cache.dtype is dtype
+            and v_cache.dtype is dtype and positions.dtype is torch.int32 and slots.dtype is torch.int32
+            and inv_freq.dtype is torch.float64 and inv_freq.dim() == 1 and k.get_device() == dev
+            and v.get_device() == dev and q_out.get_device() == dev and k_cache.get_device() == dev
+            and v_cache.get_device() == dev and positions.get_device() == dev and slots.get_device() == dev
+            and inv_freq.get_device() == dev and positions.is_contiguous() and slots.is_contiguous()
+            and inv_freq.is_contiguous()):
+        _fail(dev, (k, dtype, shape, "k", False), (v, dtype, shape, "v", False),
+              (q_out, dtype, (T, hq, D), "q_out", False), (k_cache, dtype, (None, None, hk, D), "k_cache", False),
+              (v_cache, dtype, tuple(cache), "v_cache", False), (positions, torch.int32, (T,), "positions", True),
+              (slots, torch.int32, (T,), "slots", True), (inv_freq, torch.float64, (None,), "inv_freq", True))
+    qt, qh, q1 = q.stride()
+    kt, kh, k1 = k.stride()
+    vt, vh, v1 = v.stride()
+    ot, oh, o1 = q_out.stride()
+    kcp, kcs, kch, kc1 = k_cache.stride()
+    vcp, vcs, vch, vc1 = v_cache.stride()
+    if D > 1 and not q1 == k1 == v1 == o1 == kc1 == vc1 == 1:
+        raise ValueError("the last dimension of every tensor must be contiguous")
+    args = _ROPE_ARGS.pack(dt, T, D, 2 * inv_freq.shape[0], offset, interleaved, inverse, hq, hk, scale, cache[1],
+                           cache[0], positions.data_ptr(), inv_freq.data_ptr(), slots.data_ptr(), q.data_ptr(),
+                           k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), qt,
+                           qh, kt, kh, vt, vh, ot, oh, kcp, kcs, kch, vcp, vcs, vch)
+    st = (_lib or load()).moe_rope(args, _raw_stream(dev))
     if st:
         _check(st, "moe_rope")
     return q_out
@@ -603,36 +617,43 @@ def moe_linear_int4_workspace_size(M, N, K, group, gated=False) -> int:
     return int(load().moe_linear_int4_workspace_size(M, N, K, group, 1 if gated else 0))
 
 
+@functools.lru_cache(maxsize=256)
+def _linear_workspace(M, N, K, group, gated):
+    return moe_linear_int4_workspace_size(M, N, K, group, gated)
+
+
 def moe_linear_int4(x, w, w_scale, gated=False, out=None, workspace=None):
     """x [M, K] (bf16 / fp16) times 4-bit weights w uint8 [N, K/2] with w_scale fp32 [N, K/group]: [M, N].
 
     gated: w holds 2N rows, gate rows first; SiLU(gate) * up of shape [M, N].  See include/gbmoe.h.
     """
+    dtype = x.dtype
     dt = _float_dtype(x, "x", (0, 1))
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError("x must be [M, K] with contiguous rows")
-    _need(w, torch.uint8, "w")
-    _need(w_scale, torch.float32, "w_scale")
-    M, K = x.shape
-    rows, half = w.shape
-    groups = w_scale.shape[1]
-    if half * 2 != K or w_scale.shape[0] != rows or groups == 0 or K % groups or (gated and rows % 2):
-        raise ValueError("inconsistent shapes")
+    dev = x.get_device()
+    if x.dim() != 2 or w.dim() != 2 or w_scale.dim() != 2:
+        raise ValueError("x, w and w_scale must have two dimensions")
+    (M, K), (rows, half), (srows, groups) = x.shape, w.shape, w_scale.shape
     N = rows // 2 if gated else rows
     if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=x.device)
-    elif out.dtype != x.dtype or not out.is_cuda or tuple(out.shape) != (M, N) or (N > 1 and out.stride(1) != 1):
-        raise ValueError("out must be [M, N] of x's type with contiguous rows")
-    lib, group, ws, ws_bytes = load(), K // groups, 0, 0
+        out = torch.empty((M, N), dtype=dtype, device=x.device)
+    xs, x1 = x.stride()
+    os_, o1 = out.stride()
+    if not (half * 2 == K and srows == rows and groups > 0 and K % groups == 0 and (not gated or rows % 2 == 0)
+            and w.dtype is torch.uint8 and w_scale.dtype is torch.float32 and w.get_device() == dev
+            and w_scale.get_device() == dev and w.is_contiguous() and w_scale.is_contiguous() and out.dtype is dtype
+            and out.get_device() == dev and out.shape == (M, N) and (x1 == 1 or K == 1) and (o1 == 1 or N == 1)):
+        _fail(dev, (x, dtype, (M, K), "x", False), (w, torch.uint8, (None, K // 2), "w", True),
+              (w_scale, torch.float32, (rows, None), "w_scale", True), (out, dtype, (M, N), "out", False))
+    group, ws, ws_bytes = K // groups, 0, 0
     if workspace is None and (M > 8 or K > 8192):
-        n = lib.moe_linear_int4_workspace_size(M, N, K, group, 1 if gated else 0)
+        n = _linear_workspace(M, N, K, group, bool(gated))
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel()
-    st = lib.moe_linear_int4(dt, x.data_ptr(), x.stride(0) if M > 1 else K, w.data_ptr(), w_scale.data_ptr(), M, N, K,
-                             group, 1 if gated else 0, out.data_ptr(), out.stride(0) if M > 1 else N, ws, ws_bytes,
-                             _raw_stream(x))
+    st = (_lib or load()).moe_linear_int4(dt, x.data_ptr(), xs if M > 1 else K, w.data_ptr(), w_scale.data_ptr(), M, N,
+                                          K, group, 1 if gated else 0, out.data_ptr(), os_ if M > 1 else N, ws,
+                                          ws_bytes, _raw_stream(dev))
     if st:
         _check(st, "moe_linear_int4")
     return out
@@ -640,6 +661,14 @@ def moe_linear_int4(x, w, w_scale, gated=False, out=None, workspace=None):
 
 def moe_tree_attention_workspace_size(nodes, batch, q_heads, k_heads, dim) -> int:
     return int(load().moe_tree_attention_workspace_size(nodes, batch, q_heads, k_heads, dim))
+
+
+@functools.lru_cache(maxsize=256)
+def _tree_workspace(nodes, batch, q_heads, k_heads, dim):
+    n = moe_tree_attention_workspace_size(nodes, batch, q_heads, k_heads, dim)
+    if n == 0:
+        raise MoEError(2, "moe_tree_attention_workspace_size", "unsupported sizes")
+    return n
 
 
 def moe_tree_attention(q, k_cache, v_cache, block_table, context_lens, node_offsets, tree_mask=None, scale=None,
@@ -650,43 +679,47 @@ def moe_tree_attention(q, k_cache, v_cache, block_table, context_lens, node_offs
     context_lens int32 [batch]; node_offsets int32 [batch + 1]; tree_mask int64 / uint64 [nodes] (None: chains);
     scale defaults to dim ** -0.5.
     """
+    dtype = q.dtype
     dt = _float_dtype(q, "q", (0, 1))
-    qs = _rows3(q, q.dtype, "q")
+    dev = q.get_device()
+    if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("q must be [nodes, q_heads, dim], the caches [pages, page_size, k_heads, dim], "
+                         "block_table [batch, pages of a sequence]")
     N, hq, D = q.shape
-    kc, vc = _pages4(k_cache, q.dtype, "k_cache"), _pages4(v_cache, q.dtype, "v_cache")
-    pages, page, hk, dk = k_cache.shape
-    if k_cache.shape != v_cache.shape or dk != D:
-        raise ValueError("k_cache and v_cache must be [pages, page_size, k_heads, dim]")
-    if not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2:
-        raise ValueError("block_table must be an int32 CUDA tensor [batch, pages of a sequence]")
+    pages, page, hk, dk = cache = k_cache.shape
     B, width = block_table.shape
-    if width > 1 and block_table.stride(1) != 1:
-        raise ValueError("the rows of block_table must be contiguous")
-    for t, n, name in ((context_lens, B, "context_lens"), (node_offsets, B + 1, "node_offsets")):
-        if not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or t.numel() != n:
-            raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of {n} entries")
+    if out is None:
+        out = torch.empty((N, hq, D), dtype=dtype, device=q.device)
+    qt, qh, q1 = q.stride()
+    ot, oh, o1 = out.stride()
+    kp, ks, kh, k1 = k_cache.stride()
+    vp, vs, vh, v1 = v_cache.stride()
+    tld, t1 = block_table.stride()
+    i32 = torch.int32
+    if not (dk == D and cache == v_cache.shape and out.shape == q.shape and q1 == o1 == k1 == v1 == 1
+            and (t1 == 1 or width <= 1) and k_cache.dtype is dtype and v_cache.dtype is dtype and out.dtype is dtype
+            and block_table.dtype is i32 and context_lens.dtype is i32 and node_offsets.dtype is i32
+            and context_lens.shape == (B,) and node_offsets.shape == (B + 1,) and context_lens.is_contiguous()
+            and node_offsets.is_contiguous() and k_cache.get_device() == dev and v_cache.get_device() == dev
+            and out.get_device() == dev and block_table.get_device() == dev and context_lens.get_device() == dev
+            and node_offsets.get_device() == dev):
+        _fail(dev, (q, dtype, (N, hq, D), "q", False), (out, dtype, (N, hq, D), "out", False),
+              (k_cache, dtype, (None, None, None, D), "k_cache", False), (v_cache, dtype, tuple(cache), "v_cache", False),
+              (block_table, i32, (B, width), "block_table", False), (context_lens, i32, (B,), "context_lens", True),
+              (node_offsets, i32, (B + 1,), "node_offsets", True))
     mask = 0
     if tree_mask is not None:
-        if (not tree_mask.is_cuda or tree_mask.dtype not in (torch.int64, torch.uint64)
-                or not tree_mask.is_contiguous() or tree_mask.numel() != N):
+        if not ((tree_mask.dtype is torch.int64 or tree_mask.dtype is torch.uint64) and tree_mask.shape == (N,)
+                and tree_mask.is_contiguous() and tree_mask.get_device() == dev):
             raise ValueError("tree_mask must be a contiguous 64-bit CUDA tensor with one word a node")
         mask = tree_mask.data_ptr()
-    if out is None:
-        out = torch.empty((N, hq, D), dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    os_ = _rows3(out, q.dtype, "out")
-    lib = load()
     if workspace is None:
-        n = lib.moe_tree_attention_workspace_size(N, B, hq, hk, D) if B else 256
-        if n == 0:
-            raise MoEError(2, "moe_tree_attention_workspace_size", "unsupported sizes")
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    args = _TREE_ARGS.pack(dt, N, B, hq, hk, D, page, pages, width, D ** -0.5 if scale is None else scale,
-                           block_table.stride(0), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                           block_table.data_ptr(), context_lens.data_ptr(), node_offsets.data_ptr(), mask,
-                           out.data_ptr(), qs[0], qs[1], os_[0], os_[1], kc[0], kc[1], kc[2], vc[0], vc[1], vc[2])
-    st = lib.moe_tree_attention(args, workspace.data_ptr(), workspace.numel(), _raw_stream(q))
+        workspace = torch.empty(_tree_workspace(N, B, hq, hk, D) if B else 256, dtype=torch.uint8, device=q.device)
+    args = _TREE_ARGS.pack(dt, N, B, hq, hk, D, page, pages, width, D ** -0.5 if scale is None else scale, tld,
+                           q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+                           context_lens.data_ptr(), node_offsets.data_ptr(), mask, out.data_ptr(), qt, qh, ot, oh, kp,
+                           ks, kh, vp, vs, vh)
+    st = (_lib or load()).moe_tree_attention(args, workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
     if st:
         _check(st, "moe_tree_attention")
     return out
@@ -707,41 +740,47 @@ def moe_verify_draft(target_probs, tokens, node_offsets, coins, last_coins, max_
     coins fp32 [nodes + batch]; last_coins fp32 [batch]; draft_probs fp32 [nodes, vocab] (chains only).
     Returns (out_tokens [batch, max_nodes + 1], path [batch, max_nodes], accepted [batch]), int32.
     """
-    if not target_probs.is_cuda or target_probs.dtype != torch.float32 or target_probs.dim() != 2:
-        raise ValueError("target_probs must be an fp32 CUDA tensor [nodes + batch, vocab]")
-    N, B, V = tokens.numel(), last_coins.numel(), target_probs.shape[1]
-    if target_probs.shape[0] != N + B or (V > 1 and target_probs.stride(1) != 1):
-        raise ValueError("target_probs must be [nodes + batch, vocab] with contiguous rows")
-    for t, n, dtype, name in ((tokens, N, torch.int32, "tokens"), (node_offsets, B + 1, torch.int32, "node_offsets"),
-                              (coins, N + B, torch.float32, "coins"), (last_coins, B, torch.float32, "last_coins")):
-        if not t.is_cuda or t.dtype != dtype or not t.is_contiguous() or t.numel() != n:
-            raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of {n} entries")
+    dev = target_probs.get_device()
+    if target_probs.dim() != 2:
+        raise ValueError("target_probs must be [nodes + batch, vocab]")
+    (R, V), N, B = target_probs.shape, tokens.numel(), last_coins.numel()
+    device, i32, f32 = target_probs.device, torch.int32, torch.float32
+    if out_tokens is None:
+        out_tokens = torch.empty((B, max_nodes + 1), dtype=i32, device=device)
+    if path is None:
+        path = torch.empty((B, max_nodes), dtype=i32, device=device)
+    if accepted is None:
+        accepted = torch.empty((B,), dtype=i32, device=device)
+    ts, t1 = target_probs.stride()
+    if not (dev >= 0 and R == N + B and (t1 == 1 or V == 1) and target_probs.dtype is f32 and tokens.dtype is i32
+            and node_offsets.dtype is i32 and coins.dtype is f32 and last_coins.dtype is f32
+            and tokens.shape == (N,) and node_offsets.shape == (B + 1,) and coins.shape == (R,)
+            and last_coins.shape == (B,) and tokens.is_contiguous() and node_offsets.is_contiguous()
+            and coins.is_contiguous() and last_coins.is_contiguous() and tokens.get_device() == dev
+            and node_offsets.get_device() == dev and coins.get_device() == dev and last_coins.get_device() == dev
+            and out_tokens.shape == (B, max_nodes + 1) and path.shape == (B, max_nodes) and accepted.shape == (B,)
+            and out_tokens.dtype is i32 and path.dtype is i32 and accepted.dtype is i32
+            and out_tokens.is_contiguous() and path.is_contiguous() and accepted.is_contiguous()
+            and out_tokens.get_device() == dev and path.get_device() == dev and accepted.get_device() == dev):
+        _fail(dev, (target_probs, f32, (N + B, None), "target_probs", False), (tokens, i32, (N,), "tokens", True),
+              (node_offsets, i32, (B + 1,), "node_offsets", True), (coins, f32, (N + B,), "coins", True),
+              (last_coins, f32, (B,), "last_coins", True), (out_tokens, i32, (B, max_nodes + 1), "out_tokens", True),
+              (path, i32, (B, max_nodes), "path", True), (accepted, i32, (B,), "accepted", True))
     pp = dp = ds = 0
     if parents is not None:
-        if not parents.is_cuda or parents.dtype != torch.int32 or not parents.is_contiguous() or parents.numel() != N:
-            raise ValueError("parents must be a contiguous int32 CUDA tensor with one entry a node")
+        if not (parents.dtype is i32 and parents.shape == (N,) and parents.is_contiguous()
+                and parents.get_device() == dev):
+            _fail_tensor(parents, dev, i32, (N,), "parents", True)
         pp = parents.data_ptr()
     if draft_probs is not None:
-        if (not draft_probs.is_cuda or draft_probs.dtype != torch.float32 or tuple(draft_probs.shape) != (N, V)
-                or (V > 1 and draft_probs.stride(1) != 1)):
-            raise ValueError("draft_probs must be an fp32 CUDA tensor [nodes, vocab] with contiguous rows")
+        if not (draft_probs.dtype is f32 and draft_probs.shape == (N, V) and draft_probs.get_device() == dev
+                and (V == 1 or draft_probs.stride(1) == 1)):
+            _fail_tensor(draft_probs, dev, f32, (N, V), "draft_probs", False)
         dp, ds = draft_probs.data_ptr(), max(draft_probs.stride(0), V)
-    dev = target_probs.device
-    for name, t, shape in (("out_tokens", out_tokens, (B, max_nodes + 1)), ("path", path, (B, max_nodes)),
-                           ("accepted", accepted, (B,))):
-        if t is not None:
-            _need(t, torch.int32, name)
-            if tuple(t.shape) != shape:
-                raise ValueError(f"{name} must be {list(shape)}")
-    if out_tokens is None:
-        out_tokens = torch.empty((B, max_nodes + 1), dtype=torch.int32, device=dev)
-    if path is None:
-        path = torch.empty((B, max_nodes), dtype=torch.int32, device=dev)
-    if accepted is None:
-        accepted = torch.empty(B, dtype=torch.int32, device=dev)
-    st = load().moe_verify_draft(target_probs.data_ptr(), max(target_probs.stride(0), V), dp, ds, tokens.data_ptr(), pp,
-                                 node_offsets.data_ptr(), coins.data_ptr(), last_coins.data_ptr(), B, N, V, max_nodes,
-                                 out_tokens.data_ptr(), path.data_ptr(), accepted.data_ptr(), _raw_stream(target_probs))
+    st = (_lib or load()).moe_verify_draft(target_probs.data_ptr(), max(ts, V), dp, ds, tokens.data_ptr(), pp,
+                                           node_offsets.data_ptr(), coins.data_ptr(), last_coins.data_ptr(), B, N, V,
+                                           max_nodes, out_tokens.data_ptr(), path.data_ptr(), accepted.data_ptr(),
+                                           _raw_stream(dev))
     if st:
         _check(st, "moe_verify_draft")
     return out_tokens, path, accepted
