@@ -591,7 +591,7 @@ moe_status_t moe_read_tree_status(const void* workspace, int32_t status_out[2], 
  *    none does, the next token is a sample of the row without the children.
  * After the last kept node the next token is a sample of its row.  A sample of w
  * is the first x with w_0 + .. + w_x > last_coins[b] * sum(w), sums being exact
- * in units of 2^-56 (where a residual has no weight: of the target row).
+ * in units of 2^-60 (where a residual has no weight: of the target row).
  *   target_probs fp32 [nodes + batch, vocab], draft_probs fp32 [nodes, vocab]
  *   tokens, parents int32 [nodes], parents[j] < j counted from the sequence's
  *                first node, -1 for the committed end
@@ -600,7 +600,7 @@ moe_status_t moe_read_tree_status(const void* workspace, int32_t status_out[2], 
  *   path         int32 [batch, max_nodes] out: kept nodes in order, then -1
  *   accepted     int32 [batch] out: number of kept nodes; -1 (and no tokens) for
  *                a sequence with bad offsets, tokens or parents, or whose row has
- *                no weight or a sum above 128
+ *                no weight or a sum above 8
  * Probabilities above 1 count as 1, negative ones and NaN as 0.
  */
 moe_status_t moe_verify_draft(const float* target_probs, int64_t target_stride, const float* draft_probs,

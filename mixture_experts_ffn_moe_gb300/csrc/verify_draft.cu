@@ -9,9 +9,13 @@
 // Where all of a path is kept, the next token is a sample of the last row.  A sample is the first token x with
 // sum_{i <= x} w_i > u * sum_i w_i.
 //
-// Arithmetic.  coin * q is exact in 64 bits.  The weights become 56-bit fixed-point integers (p * 2^56 rounded to
-// nearest), so their sums are exact, do not depend on the order of the threads, and the comparison with the
-// threshold is one of integers: FP64 sums would be equally exact but run at a sixtieth of the integer rate here.
+// Arithmetic.  coin * q is exact in 64 bits.  The weights count as integers in units of 2^-60 (rounded to nearest;
+// any p of 2^-37 and more is a whole number of them), so their sums are exact, do not depend on the order of the
+// threads, and the comparison with the threshold is one of integers.  The integers are not formed one by one: adding
+// 1, 1.5 * 2^-23 and 1.5 * 2^-37 to p and to what each sum leaves over puts three pieces of the integer into the low
+// mantissa bits of three floats, whose bit patterns are added up as 32-bit integers (the constants' share is known and
+// taken off at the end).  That is 8 additions of floats and 3 of integers a weight; shifting the mantissa into place
+// took about 45 instructions and bound the kernel, and FP64 runs at a sixtieth of the fp32 rate here.
 //
 // Bound: the one row (two with q) of the vocabulary that is sampled from; everything else is a gather of at most
 // 64 probabilities.  In practice a chain of dependent reads: offsets, nodes, their probabilities, the row, and the
@@ -49,13 +53,51 @@ struct VerifyArgs {
   int N, V, max_nodes;
 };
 
-// p * 2^56 rounded to nearest for p in [0, 1]; larger values count as 1, negative ones and NaN as 0.
-__device__ __forceinline__ uint64_t fixed56(float p) {
-  p = fminf(p > 0.f ? p : 0.f, 1.f);
-  const uint32_t b = __float_as_uint(p);
-  const uint32_t d = 127u - (b >> 23);  // p = m * 2^(-23 - d)
-  const uint64_t m = static_cast<uint64_t>((b & 0x7fffffu) | 0x800000u) << 34;
-  return d > 58 ? 0ull : ((m >> d) + 1) >> 1;
+// The sum of weights as three 32-bit sums of bit patterns (up to 32 of them).
+struct Levels {
+  uint32_t a = 0, b = 0, c = 0;
+};
+constexpr float kC2 = 0x1.8p-23f, kC3 = 0x1.8p-37f;  // spacing 2^-46 and 2^-60
+__device__ __forceinline__ void split3(float p, uint32_t& x, uint32_t& y, uint32_t& z) {
+  const float t = __fadd_rn(p, 1.f), r = __fadd_rn(p, -__fadd_rn(t, -1.f)), u = __fadd_rn(r, kC2);
+  x = __float_as_uint(t);
+  y = __float_as_uint(u);
+  z = __float_as_uint(__fadd_rn(__fadd_rn(r, -__fadd_rn(u, -kC2)), kC3));
+}
+// Probabilities above 1 count as 1, negative ones and NaN as 0.
+__device__ __forceinline__ float clamp01(float p) { return fminf(fmaxf(p, 0.f), 1.f); }
+// Adds p, or max(p - q, 0).
+template <bool Q>
+__device__ __forceinline__ void add_weight(Levels& l, float p, float q) {
+  uint32_t x, y, z;
+  if constexpr (Q) {
+    const bool more = p > q;
+    split3(more ? p : 0.f, x, y, z);
+    uint32_t x2, y2, z2;
+    split3(more ? q : 0.f, x2, y2, z2);
+    l.a += x - x2;
+    l.b += y - y2;
+    l.c += z - z2;
+  } else {
+    split3(p, x, y, z);
+    l.a += x;
+    l.b += y;
+    l.c += z;
+  }
+}
+// The integer of a sum of n weights.
+template <bool Q>
+__device__ __forceinline__ uint64_t integer(const Levels& l, int n) {
+  const uint32_t k = Q ? 0u : static_cast<uint32_t>(n);
+  const int64_t a = static_cast<int32_t>(l.a - k * 0x3f800000u);
+  const int64_t b = static_cast<int32_t>(l.b - k * 0x34400000u);  // kC2
+  const int64_t c = static_cast<int32_t>(l.c - k * 0x2d400000u);  // kC3
+  return static_cast<uint64_t>((a << 37) + (b << 14) + c);
+}
+__device__ __forceinline__ uint64_t integer_of(float p) {
+  Levels l;
+  add_weight<false>(l, p, 0.f);
+  return integer<false>(l, 1);
 }
 
 // u * 2^64 (rounded down) for u in [0, 1); what lies outside is brought to the nearest end.
@@ -66,43 +108,125 @@ __device__ __forceinline__ uint64_t fraction64(float u) {
   return e >= 0 ? m << e : (e < -63 ? 0 : m >> -e);
 }
 
-__device__ __forceinline__ uint64_t weight(float p, float q, bool has_q) {
-  const uint64_t a = fixed56(p);
-  if (!has_q) return a;
-  const uint64_t b = fixed56(q);
-  return a > b ? a - b : 0ull;
-}
-
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// A lane's 32 weights of the tile at `base`, all loads in flight: VEC neighbours of every 32 * VEC tokens.  fs: the
-// plain sum of p, to tell rows that are no probabilities.
-template <int VEC>
-__device__ __forceinline__ void load_tile(const float* p, const float* q, int base, int V, int lane, uint64_t (&w)[32], float& fs) {
-  float a[32], b[32];
+// A lane's 32 probabilities of the tile at `base` (clamped), all loads in flight: VEC neighbours of every 32 * VEC
+// tokens.
+template <int VEC, bool Q>
+__device__ __forceinline__ void load_tile(const float* p, const float* q, int base, int V, int lane, float (&a)[32], float (&b)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; i += VEC) {
     const int at = base + (i / VEC * 32 + lane) * VEC;
     if constexpr (VEC == 4) {
       const bool in = at + 3 < V;  // V is a multiple of 4
       const float4 x = in ? __ldg(reinterpret_cast<const float4*>(p + at)) : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float4 y = in && q ? __ldg(reinterpret_cast<const float4*>(q + at)) : make_float4(0.f, 0.f, 0.f, 0.f);
       a[i] = x.x; a[i + 1] = x.y; a[i + 2] = x.z; a[i + 3] = x.w;
-      b[i] = y.x; b[i + 1] = y.y; b[i + 2] = y.z; b[i + 3] = y.w;
+      if constexpr (Q) {
+        const float4 y = in ? __ldg(reinterpret_cast<const float4*>(q + at)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        b[i] = y.x; b[i + 1] = y.y; b[i + 2] = y.z; b[i + 3] = y.w;
+      }
     } else {
       a[i] = at < V ? __ldg(p + at) : 0.f;
-      b[i] = at < V && q ? __ldg(q + at) : 0.f;
+      if constexpr (Q) b[i] = at < V ? __ldg(q + at) : 0.f;
     }
   }
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
-    w[i] = weight(a[i], b[i], q != nullptr);
-    fs += a[i] > 0.f ? fminf(a[i], 1.f) : 0.f;
+    a[i] = clamp01(a[i]);
+    if constexpr (Q) b[i] = clamp01(b[i]);
   }
+}
+
+// The sum of a tile's weights in units of 2^-60 (a lane's share), and the plain sum of its probabilities into fs.
+template <int VEC, bool Q>
+__device__ __forceinline__ uint64_t sum_tile(const float* p, const float* q, int base, int V, int lane, float& fs) {
+  float a[32], b[32];
+  load_tile<VEC, Q>(p, q, base, V, lane, a, b);
+  Levels l;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    add_weight<Q>(l, a[i], b[i]);
+    fs += a[i];
+  }
+  return integer<Q>(l, 32);
+}
+
+// The first token of the tile at `base` with before + (running sum) > level, by a whole warp; -1 if there is none.
+// gone[0..n): tokens of the tile that count nothing.
+template <int VEC, bool Q>
+__device__ __forceinline__ int search_tile(const float* p, const float* q, int base, int V, int lane, uint64_t before, uint64_t level,
+                                           const int* tok, const int* par, int n, int stop) {
+  constexpr int NG = 32 / VEC;
+  float a[32], b[32];
+  load_tile<VEC, Q>(p, q, base, V, lane, a, b);
+  for (int j = 0; j < n; ++j)
+    if (par[j] == stop && tok[j] >= base && tok[j] < base + kVTile) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (base + (i / VEC * 32 + lane) * VEC + i % VEC == tok[j]) a[i] = 0.f;
+    }
+  // tokens in order: groups of 32 * VEC, in them VEC a lane.  The groups' sums do not wait for each other.
+  int at = -1;
+  float ga[VEC], gb[VEC];
+#pragma unroll
+  for (int i0 = 0; i0 < NG; i0 += 8) {
+    uint64_t grp[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      Levels l;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) add_weight<Q>(l, a[(i0 + i) * VEC + j], b[(i0 + i) * VEC + j]);
+      grp[i] = integer<Q>(l, VEC);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) grp[i] += __shfl_xor_sync(0xffffffffu, grp[i], o);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (at >= 0) continue;
+      if (before + grp[i] > level) {
+        at = i0 + i;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          ga[j] = a[(i0 + i) * VEC + j];
+          if constexpr (Q) gb[j] = b[(i0 + i) * VEC + j];
+        }
+      } else {
+        before += grp[i];
+      }
+    }
+  }
+  if (at < 0) return -1;
+  uint64_t w[VEC], run = 0;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    Levels l;
+    add_weight<Q>(l, ga[j], gb[j]);
+    w[j] = integer<Q>(l, 1);
+    run += w[j];
+  }
+  const uint64_t own = run;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t up = __shfl_up_sync(0xffffffffu, run, o);
+    if (lane >= o) run += up;
+  }
+  const unsigned hit = __ballot_sync(0xffffffffu, before + run > level);
+  const int who = __ffs(hit) - 1;  // the group's last lane at the latest
+  uint64_t sum = before + run - own;
+  int x = base + (at * 32 + lane) * VEC;
+  bool here = false;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    sum += w[j];
+    if (!here && sum > level) { here = true; x += j; }
+  }
+  return __shfl_sync(0xffffffffu, x, who);
 }
 
 struct Shared {
@@ -110,7 +234,8 @@ struct Shared {
   float p[64];
   unsigned char again[64];
   unsigned long long taken, okmask;
-  int n, bad, stop, count;
+  uint64_t share[64];  // p in units of 2^-60
+  int bad;
   uint64_t warp_tot[kVWarps];
   float warp_f[kVWarps];
   uint64_t cta_tot[kMaxCluster];
@@ -132,7 +257,7 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyArgs a) {
   const int lo = a.offsets[b], hi = a.offsets[b + 1];
   const int n = hi - lo;
   const bool bad_range = lo < 0 || hi < lo || hi > a.N || n > a.max_nodes;
-  if (tid == 0) { sh.bad = bad_range; sh.taken = 0; sh.found = 0x7fffffff; }
+  if (tid == 0) { sh.bad = bad_range; sh.taken = 0; sh.okmask = 0; sh.found = -1; }
   __syncthreads();
   const long long row0 = static_cast<long long>(lo) + b;
   float coin = 0.f, q = 0.f;
@@ -146,6 +271,7 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyArgs a) {
     if (ok) {
       const float p = a.target[(row0 + par + 1) * a.ldt + tok];
       sh.p[tid] = p > 0.f ? p : 0.f;
+      sh.share[tid] = integer_of(clamp01(p));
       coin = a.coins[row0 + par + 1];
       if (a.draft) q = a.draft[(lo + tid) * a.ldd + tok];
     }
@@ -163,31 +289,24 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyArgs a) {
     if (a.draft) {
       taken = static_cast<double>(coin) * static_cast<double>(q) < static_cast<double>(sh.p[tid]);
     } else {
-      double before = 0.0;
+      uint64_t before = 0;  // the earlier siblings' shares
       for (int j = 0; j < tid; ++j)
-        if (sh.par[j] == sh.par[tid] && !sh.again[j]) before += static_cast<double>(sh.p[j]);
-      const double c = static_cast<double>(coin);
-      taken = !sh.again[tid] && c >= before && c < before + static_cast<double>(sh.p[tid]);
+        if (sh.par[j] == sh.par[tid] && !sh.again[j]) before += sh.share[j];
+      const uint64_t c = fraction64(coin) >> 4;
+      taken = !sh.again[tid] && c >= before && c < before + sh.share[tid];
     }
     if (taken) atomicOr(&sh.taken, 1ull << tid);
   }
   __syncthreads();
-  if (tid == 0) {
-    unsigned long long ok = 0;
-    int stop = -1, count = 0;
-    if (!bad) {
-      const unsigned long long taken = sh.taken;
-      for (int j = 0; j < n; ++j) {
-        const int p = sh.par[j];
-        if (((taken >> j) & 1) && (p < 0 || ((ok >> p) & 1))) { ok |= 1ull << j; stop = j; ++count; }
-      }
-    }
-    sh.okmask = ok;
-    sh.stop = stop;
-    sh.count = count;
+  if (!bad && tid < n) {  // kept: taken, and so is every ancestor
+    const unsigned long long taken = sh.taken;
+    int up = tid;
+    while (up >= 0 && ((taken >> up) & 1)) up = sh.par[up];
+    if (up < 0) atomicOr(&sh.okmask, 1ull << tid);
   }
   __syncthreads();
-  const int stop = sh.stop, count = sh.count;
+  // the kept nodes are one path, so the last one is the deepest
+  const int stop = 63 - __clzll(static_cast<long long>(sh.okmask)), count = __popcll(sh.okmask);
 
   // ---- the row that the next token is drawn from
   const float* prow = a.target + (row0 + stop + 1) * a.ldt;
@@ -203,14 +322,11 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyArgs a) {
     float fs = 0.f;
     uint64_t mine = 0;  // lane 0: the warp's tiles
     for (int t = warp; t < my_tiles; t += kVWarps) {
-      uint64_t w[32];
-      uint64_t sum = 0;
-      load_tile<VEC>(prow, use_q ? qrow : nullptr, (tile0 + t) * kVTile, a.V, lane, w, fs);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) sum += w[i];
+      const int at = (tile0 + t) * kVTile;
+      uint64_t sum = use_q ? sum_tile<VEC, true>(prow, qrow, at, a.V, lane, fs) : sum_tile<VEC, false>(prow, nullptr, at, a.V, lane, fs);
       if (!a.draft && residual)
         for (int j = lane; j < n; j += 32)
-          if (sh.par[j] == stop && !sh.again[j] && sh.tok[j] / kVTile == tile0 + t) sum -= fixed56(sh.p[j]);
+          if (sh.par[j] == stop && !sh.again[j] && sh.tok[j] / kVTile == tile0 + t) sum -= sh.share[j];
       sum = warp_sum64(sum);
       if (lane == 0) tile_sum[t] = sum;
       mine += sum;
@@ -235,7 +351,7 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyArgs a) {
       total += sh.cta_tot[r];
       f += sh.cta_f[r];
     }
-    if (!(f <= 128.f)) break;  // not probabilities: 56 bits would overflow
+    if (!(f <= 8.f)) break;  // not probabilities: 64 bits would overflow at 16
     if (total != 0) {
       // floor(u * total) for u in [0, 1): x is the first token whose running sum is above it
       const uint64_t level = __umul64hi(fraction64(a.last[b]), total);
@@ -258,46 +374,10 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyArgs a) {
           }
           before += __shfl_sync(0xffffffffu, run, 31);
         }
-        uint64_t w[32];
-        const int base = (tile0 + t) * kVTile;
-        load_tile<VEC>(prow, use_q ? qrow : nullptr, base, a.V, lane, w, fs);
-        if (!a.draft && residual)
-          for (int j = 0; j < n; ++j)
-            if (sh.par[j] == stop && sh.tok[j] / kVTile == tile0 + t) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (base + (i / VEC * 32 + lane) * VEC + i % VEC == sh.tok[j]) w[i] = 0;
-            }
-        // tokens in order: groups of 32 * VEC, in them VEC a lane
-        bool found = false;
-#pragma unroll
-        for (int i0 = 0; i0 < 32; i0 += VEC) {
-          uint64_t own = 0;
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) own += w[i0 + i];
-          uint64_t run = own;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t up = __shfl_up_sync(0xffffffffu, run, o);
-            if (lane >= o) run += up;
-          }
-          const unsigned hit = found ? 0u : __ballot_sync(0xffffffffu, before + run > level);
-          if (hit) {
-            found = true;
-            if (lane == __ffs(hit) - 1) {
-              uint64_t at = before + run - own;
-              int x = base + (i0 / VEC * 32 + lane) * VEC;
-              bool here = false;
-#pragma unroll
-              for (int i = 0; i < VEC; ++i) {
-                at += w[i0 + i];
-                if (!here && at > level) { here = true; x += i; }
-              }
-              cluster.map_shared_rank(&sh, 0)->found = x;
-            }
-          }
-          before += __shfl_sync(0xffffffffu, run, 31);
-        }
+        const int at = (tile0 + t) * kVTile, gone = a.draft || !residual ? 0 : n;
+        const int x = use_q ? search_tile<VEC, true>(prow, qrow, at, a.V, lane, before, level, sh.tok, sh.par, gone, stop)
+                            : search_tile<VEC, false>(prow, nullptr, at, a.V, lane, before, level, sh.tok, sh.par, gone, stop);
+        if (lane == 0) cluster.map_shared_rank(&sh, 0)->found = x;
       }
     }
     cluster.sync();  // found has arrived; the sums may be written again

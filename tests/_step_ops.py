@@ -90,14 +90,21 @@ def tree_ref(q, k_cache, v_cache, table, ctx, offs, masks, scale):
     return out, bound
 
 
-def fixed56(p):
-    """p * 2^56 rounded to nearest (ties up), for float32 p clamped to [0, 1]; python ints."""
+def fixed60(p):
+    """p * 2^60 rounded to nearest even, for float32 p clamped to [0, 1]; python ints."""
     p = np.nan_to_num(np.asarray(p, dtype=np.float32), nan=0.0, posinf=1.0, neginf=0.0)
     p = np.clip(p, 0.0, 1.0)
     m, e = np.frexp(p.astype(np.float64))
     mant = (m * 2.0 ** 24).astype(np.int64)  # exact: 24 bits
-    sh = e.astype(np.int64) - 24 + 56
-    return [((int(a) << int(s)) if s >= 0 else ((int(a) << 1 >> int(-s)) + 1) >> 1) if a else 0 for a, s in zip(mant, sh)]
+    out = []
+    for a, s in zip(mant.tolist(), (e.astype(np.int64) - 24 + 60).tolist()):
+        if s >= 0:
+            out.append(a << s)
+        else:
+            half, v = 1 << (-s - 1), a >> -s
+            rest = a - (v << -s)
+            out.append(v + (rest > half or (rest == half and v & 1)))
+    return out
 
 
 def verify_ref(target, tokens, offs, coins, last, max_nodes, parents=None, draft=None):
@@ -114,22 +121,22 @@ def verify_ref(target, tokens, offs, coins, last, max_nodes, parents=None, draft
             row = target[lo + b + node + 1]
             coin = float(coins[lo + b + node + 1])
             kids = [j for j in range(n) if up[j] == node]
-            found, w = None, fixed56(row)
+            found, w = None, fixed60(row)
             if draft is not None:
                 if kids:
                     j = kids[0]
                     if coin * float(draft[lo + j][tok[j]]) < float(row[tok[j]]):
                         found = j
                     else:
-                        w = [max(a - c, 0) for a, c in zip(w, fixed56(draft[lo + j].numpy()))]
+                        w = [max(a - c, 0) for a, c in zip(w, fixed60(draft[lo + j].numpy()))]
             else:
-                share, seen = 0.0, set()
+                share, seen, coin60 = 0, set(), int(math.floor(coin * 2.0 ** 60))  # exact: 24 bits
                 for j in kids:
                     if tok[j] in seen:
                         continue
                     seen.add(tok[j])
-                    p = max(float(row[tok[j]]), 0.0)
-                    if share <= coin < share + p:
+                    p = fixed60(row[tok[j]:tok[j] + 1])[0]
+                    if share <= coin60 < share + p:
                         found = j
                         break
                     share += p
@@ -140,7 +147,7 @@ def verify_ref(target, tokens, offs, coins, last, max_nodes, parents=None, draft
             kept.append(found)
             node = found
         if sum(w) == 0:
-            w = fixed56(row)
+            w = fixed60(row)
         total = sum(w)
         if total == 0:
             acc[b] = -1

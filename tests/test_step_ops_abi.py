@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 import torch
 
-from _step_ops import fixed56, verify_ref
+from _step_ops import fixed60, verify_ref
 from mixture_experts_ffn_moe_gb300 import build, gbmoe
 
 P = 4096  # never dereferenced
@@ -200,4 +200,4 @@ def test_fixed_point_reference():
     for p in (0.0, 1.0, 0.5, 2.0 ** -24, 0.1, 1e-9, 1e-20, 3e-17, 2.0, -1.0, float("nan")):
         v = np.float32(p)
         exact = 0.0 if not v > 0 else min(float(v), 1.0)
-        assert abs(fixed56([v])[0] - exact * 2.0 ** 56) <= 0.5
+        assert abs(fixed60([v])[0] - exact * 2.0 ** 60) <= 0.5
