@@ -15,8 +15,10 @@
 // Work split.  A unit is (sequence, KV head, tile of rows); its cache is cut in tiles of 64 slots.  The tiles of all
 // units form one line that is divided evenly over the CTAs, whatever the lengths; where a unit is cut, the parts
 // go to the workspace as fp32 (m, l, O) and a second kernel joins them in order, so results do not depend on
-// scheduling.  Inside a CTA each warp owns 16 slots of every tile with a ring of cp.async stages of its own, so
-// warps never wait for each other inside a unit.
+// scheduling.  Inside a CTA each warp owns 16 slots of every tile with a ring of stages of its own, so warps never
+// wait for each other inside a unit.  Where pages hold a multiple of 8 slots a stage is brought by 2 or 4 TMA boxes
+// (128-byte swizzle), else slot by slot with cp.async; the next stage's block table entry is read a tile ahead.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "tree_attention.cuh"
@@ -32,6 +34,7 @@ constexpr int kTile = kAWarps * 16;  // cache slots a tile
 
 template <int D> struct TreeCfg {
   static constexpr int kRow = D * 2;                     // bytes of a cache row
+  static constexpr int kHalf = 16 * 128;                 // 64 columns of 16 slots
   static constexpr int kStage = 16 * kRow * 2;           // K and V of 16 slots
   static constexpr int S = D == 128 ? 3 : 6;             // stages a warp
   static constexpr int kRing = S * kStage;               // 24 KB a warp
@@ -39,24 +42,38 @@ template <int D> struct TreeCfg {
 
 template <int D, int RT> constexpr size_t tree_smem(int B) {
   return static_cast<size_t>(kAWarps) * (TreeCfg<D>::kRing > RT * 16 * D * 4 ? TreeCfg<D>::kRing : RT * 16 * D * 4) +
-         RT * 16 * D * 2 + (B + 1 + kAWarps) * 8 + kAWarps * (8 * 4 + RT * 16 * 8) + 1024;
+         RT * 16 * D * 2 + (B + 1 + kAWarps) * 8 + kAWarps * (8 * 4 + 8 * 8 + RT * 16 * 8) + 16 + 1024;
 }
 
-template <typename T, int D, int RT>
-__global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
+constexpr long long kLimit = 4000000000LL;  // about 2 s of SM clocks a wait
+
+template <typename T, int D, int RT, bool TMA>
+__global__ void __launch_bounds__(kAThreads, 2)
+    tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   using C = TreeCfg<D>;
   constexpr int R = RT * 16, KS = D / 16, CH = D / 8;  // rows, K steps, 16-byte chunks a row
   constexpr int kWarpBytes = C::kRing > R * D * 4 ? C::kRing : R * D * 4;
-  extern __shared__ __align__(128) unsigned char smem[];
+  extern __shared__ unsigned char raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
   unsigned char* ring = smem + (threadIdx.x >> 5) * kWarpBytes;
   unsigned char* qs = smem + kAWarps * kWarpBytes;                                       // [R][D]
   long long* prefix = reinterpret_cast<long long*>(qs + R * D * 2);                      // [B + 1], then scan scratch
-  float* ml = reinterpret_cast<float*>(prefix + a.B + 1 + kAWarps);                      // [warps][R][2]
+  uint64_t* full = reinterpret_cast<uint64_t*>(prefix + a.B + 1 + kAWarps) + (threadIdx.x >> 5) * 8;  // [S] a warp (TMA)
+  float* ml = reinterpret_cast<float*>(prefix + a.B + 1 + kAWarps + kAWarps * 8);        // [warps][R][2]
   uint32_t* okmask = reinterpret_cast<uint32_t*>(ml + kAWarps * R * 2) + (threadIdx.x >> 5) * 8;  // [S] a warp
+  int* abort_s = reinterpret_cast<int*>(ml + kAWarps * R * 2) + kAWarps * 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t ring_s = sm100::smem_addr(ring), q_s = sm100::smem_addr(qs);
+  // offset of chunk ch of slot `key` in a stage's K or V: halves of 64 columns, 128-byte rows, swizzled
+  auto chunk_at = [](int key, int ch) { return (ch >> 3) * C::kHalf + key * 128 + (((ch & 7) ^ (key & 7)) << 4); };
 
   pdl_trigger();
+  if constexpr (TMA) {
+    if (lane == 0)
+      for (int i = 0; i < C::S; ++i) sm100::mbar_init(&full[i], 1);
+    if (tid == 0) *abort_s = 0;
+    sm100::fence_barrier_init();
+  }
   pdl_wait();
   int bad_plan;
   plan_line<kAThreads>(a, prefix, prefix + a.B + 1, &bad_plan);
@@ -68,6 +85,9 @@ __global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
     for (int b = tid; b <= a.B; b += kAThreads) a.prefix[b] = prefix[b];
   }
   int bad_pages = 0;
+  int used = 0;  // stages this warp has used (TMA): stage used % S, phase used / S
+  auto stage_of = [&](int ahead) { return (used + ahead) % C::S; };
+  bool fine = true;
   long long pos = blockIdx.x * chunk;
   const long long end = pos + chunk < total ? pos + chunk : total;
   while (pos < end) {
@@ -78,37 +98,67 @@ __global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
     const T* vbase = static_cast<const T*>(a.vc) + head * a.v_head;
     const int32_t* table = a.table + b * a.table_ld;
 
-    // this warp's 16 slots of tile `it` into stage `st`
-    auto issue = [&](int it, int st) {
-      int page = -1, at = 0;
-      if (lane < 16) {
-        const int slot = it * kTile + warp * 16 + lane;
-        if (slot < L) {
-          const int pi = div_by(slot, a.page);
-          at = slot - pi * a.page.d;
-          page = __ldg(table + pi);
-          if (page < 0 || page >= a.pages) { page = -1; ++bad_pages; }
-        }
+    // The block table entry of this lane's slot of tile `it` (TMA: of its box, lane = box), a tile ahead of its use.
+    int next_page = -1, next_at = 0;
+    auto look_up = [&](int it) {
+      const int slot = it * kTile + warp * 16 + (TMA ? lane * a.box : lane);
+      next_page = -1;
+      if (it < k1 && lane < (TMA ? (a.box == 16 ? 1 : 2) : 16) && slot < L) {
+        const int pi = div_by(slot, a.page);
+        next_at = slot - pi * a.page.d;
+        next_page = __ldg(table + pi);
       }
-      const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
-      if (lane == 0) okmask[st] = ok;
-      const uint32_t base = ring_s + st * C::kStage;
+    };
+    // this warp's 16 slots of tile `it` (looked up before) into stage `st`
+    auto issue = [&](int it, int st) {
+      const int at = next_at;
+      int page = next_page;
+      if (page < 0 || page >= a.pages) {
+        const int slot = it * kTile + warp * 16 + (TMA ? lane * a.box : lane);
+        if (lane < (TMA ? (a.box == 16 ? 1 : 2) : 16) && slot < L) bad_pages += TMA ? min(a.box, L - slot) : 1;
+        page = -1;
+      }
+      look_up(it + 1);
+      if constexpr (TMA) {
+        const int pg = __shfl_sync(0xffffffffu, page, (lane & 15) >> (a.box == 16 ? 4 : 3)), sl = __shfl_sync(0xffffffffu, at, (lane & 15) >> (a.box == 16 ? 4 : 3));
+        const uint32_t ok = __ballot_sync(0xffffffffu, lane < 16 && pg >= 0 && it * kTile + warp * 16 + lane < L);
+        if (lane == 0) {
+          okmask[st] = ok;
+          sm100::mbar_arrive_expect_tx(&full[st], C::kStage);
+        }
+        __syncwarp();
+        // lanes on the first slot of a box: K and V of each half.  Page -1 is outside the tensor: zeros.
+        if (lane < 16 && (lane & (a.box - 1)) == 0) {
+          const uint32_t dst = ring_s + st * C::kStage + lane * 128;
 #pragma unroll
-      for (int i = 0; i < 16 * CH / 32; ++i) {
-        const int c = i * 32 + lane, r = c / CH, ch = c % CH;
-        const int pg = __shfl_sync(0xffffffffu, page, r), sl = __shfl_sync(0xffffffffu, at, r);
-        const bool live = pg >= 0;
-        const long long p = live ? pg : 0;
-        const uint32_t dst = base + r * C::kRow + ((ch ^ (r & 7)) << 4);
-        cp_async16(dst, kbase + p * a.k_page + sl * a.k_slot + ch * 8, live);
-        cp_async16(dst + 16 * C::kRow, vbase + p * a.v_page + sl * a.v_slot + ch * 8, live);
+          for (int h = 0; h < D / 64; ++h) {
+            sm100::tma_load_4d(dst + h * C::kHalf, &mk, &full[st], h * 64, sl, head, pg);
+            sm100::tma_load_4d(dst + 16 * C::kRow + h * C::kHalf, &mv, &full[st], h * 64, sl, head, pg);
+          }
+        }
+      } else {
+        const uint32_t ok = __ballot_sync(0xffffffffu, page >= 0);
+        if (lane == 0) okmask[st] = ok;
+        const uint32_t base = ring_s + st * C::kStage;
+#pragma unroll
+        for (int i = 0; i < 16 * CH / 32; ++i) {
+          const int c = i * 32 + lane, r = c / CH, ch = c % CH;
+          const int pg = __shfl_sync(0xffffffffu, page, r), sl = __shfl_sync(0xffffffffu, at, r);
+          const bool live = pg >= 0;
+          const long long p = live ? pg : 0;
+          const uint32_t dst = base + chunk_at(r, ch);
+          cp_async16(dst, kbase + p * a.k_page + sl * a.k_slot + ch * 8, live);
+          cp_async16(dst + 16 * C::kRow, vbase + p * a.v_page + sl * a.v_slot + ch * 8, live);
+        }
       }
     };
     __syncwarp();
+    look_up(k0);
+    int sent = 0;  // tiles of this unit
 #pragma unroll
     for (int s = 0; s < C::S - 1; ++s) {
-      if (k0 + s < k1) issue(k0 + s, s);
-      cp_commit();
+      if (k0 + s < k1) { issue(k0 + s, TMA ? stage_of(s) : s); ++sent; }
+      if constexpr (!TMA) cp_commit();
     }
 
     // the unit's rows: row r is node r / group, head r % group of the KV head's queries
@@ -146,10 +196,15 @@ __global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
       l[r][0] = l[r][1] = 0.f;
     }
 
-    int st = 0;
+    int st = TMA ? stage_of(0) : 0;
     for (int it = k0; it < k1; ++it) {
-      cp_wait<C::S - 2>();
-      __syncwarp();
+      if constexpr (TMA) {
+        fine = __all_sync(0xffffffffu, sm100::mbar_wait(&full[st], (used / C::S) & 1, abort_s, nullptr, kLimit)) != 0;
+        if (!fine) break;
+      } else {
+        cp_wait<C::S - 2>();
+        __syncwarp();
+      }
       const uint32_t kst = ring_s + st * C::kStage, vst = kst + 16 * C::kRow;
       const uint32_t ok = okmask[st];
       const int slot0 = it * kTile + warp * 16;
@@ -162,7 +217,7 @@ __global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
       for (int ks = 0; ks < KS; ++ks) {
         uint32_t kb[4];
         const int key = ((lane >> 4) << 3) + (lane & 7), ch = ks * 2 + ((lane >> 3) & 1);
-        ldm4(kst + key * C::kRow + ((ch ^ (key & 7)) << 4), kb);
+        ldm4(kst + chunk_at(key, ch), kb);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           uint32_t qa[4];
@@ -209,6 +264,17 @@ __global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
           p[r][2 + h] = Elem<T>::pack(v[2], v[3]);
         }
       }
+      unsigned char* vrows = ring + st * C::kStage + 16 * C::kRow;
+      if constexpr (TMA) {
+        if (ok != 0xffffu) {  // rows of the last page past the sequence's end hold anything
+#pragma unroll
+          for (int i = 0; i < 16 * CH / 32; ++i) {
+            const int c = i * 32 + lane, r = c / CH, ch = c % CH;
+            if (!((ok >> r) & 1)) *reinterpret_cast<uint4*>(vrows + chunk_at(r, ch)) = make_uint4(0, 0, 0, 0);
+          }
+          __syncwarp();
+        }
+      }
       if (slot0 + 16 > ctx) {
         // Drafted slots are hidden from some rows: an infinity or NaN of a hidden value would come through as
         // 0 * inf.  Such slots (rare) are added to the rows that see them one by one and cleared for the rest.
@@ -216,7 +282,7 @@ __global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
 #pragma unroll
         for (int i = 0; i < 16 * CH / 32; ++i) {
           const int c = i * 32 + lane, r = c / CH, ch = c % CH;
-          const uint4 v = *reinterpret_cast<const uint4*>(ring + st * C::kStage + 16 * C::kRow + r * C::kRow + (ch << 4));
+          const uint4 v = *reinterpret_cast<const uint4*>(vrows + chunk_at(r, ch));
           const bool nf = nonfinite2(T(), v.x) || nonfinite2(T(), v.y) || nonfinite2(T(), v.z) || nonfinite2(T(), v.w);
           if (nf && slot0 + r >= ctx) odd |= 1u << r;
         }
@@ -225,7 +291,6 @@ __global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
           const int key = __ffs(odd) - 1;
           odd &= odd - 1;
           const int node = slot0 + key - ctx;
-          unsigned char* vrow = ring + st * C::kStage + 16 * C::kRow + key * C::kRow;
           const int src = (lane & ~3) | ((key & 7) >> 1);
 #pragma unroll
           for (int r = 0; r < RT; ++r)
@@ -237,14 +302,14 @@ __global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
               if ((bits[r][h] >> node) & 1) {
 #pragma unroll
                 for (int d = 0; d < CH; ++d) {
-                  const float2 vv = Elem<T>::unpack(*reinterpret_cast<const uint32_t*>(vrow + ((d ^ (key & 7)) << 4) + t * 4));
+                  const float2 vv = Elem<T>::unpack(*reinterpret_cast<const uint32_t*>(vrows + chunk_at(key, d) + t * 4));
                   o[r][d][2 * h] += pk * vv.x;
                   o[r][d][2 * h + 1] += pk * vv.y;
                 }
               }
             }
           __syncwarp();
-          if (lane < CH) *reinterpret_cast<uint4*>(vrow + lane * 16) = make_uint4(0, 0, 0, 0);
+          if (lane < CH) *reinterpret_cast<uint4*>(vrows + chunk_at(key, lane)) = make_uint4(0, 0, 0, 0);
           __syncwarp();
         }
       }
@@ -252,21 +317,36 @@ __global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
       for (int db = 0; db < KS; ++db) {
         uint32_t vb[4];
         const int key = (((lane >> 3) & 1) << 3) + (lane & 7), ch = db * 2 + (lane >> 4);
-        ldm4t(vst + key * C::kRow + ((ch ^ (key & 7)) << 4), vb);
+        ldm4t(vst + chunk_at(key, ch), vb);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           mma_16816(T(), o[r][2 * db], p[r], vb[0], vb[1]);
           mma_16816(T(), o[r][2 * db + 1], p[r], vb[2], vb[3]);
         }
       }
+      if constexpr (TMA) {
+        if (ok != 0xffffu || slot0 + 16 > ctx) sm100::fence_proxy_async_smem();  // (rows were cleared)
+      }
       __syncwarp();
       const int nx = it + C::S - 1;
-      if (nx < k1) issue(nx, st == 0 ? C::S - 1 : st - 1);
-      cp_commit();
+      if (nx < k1) { issue(nx, st == 0 ? C::S - 1 : st - 1); ++sent; }
+      if constexpr (!TMA) cp_commit();
       st = st + 1 == C::S ? 0 : st + 1;
+      ++used;
     }
-    cp_wait<0>();
-    __syncwarp();
+    if constexpr (TMA) {
+      if (!__syncthreads_and(fine)) {  // a wait gave up: what is on its way lands before the CTA goes
+        int none = 0;
+        const int done = used;  // of this unit: sent - (stages used in it) are in flight
+        for (int i = 0; i < C::S - 1; ++i)
+          if (lane == 0 && i < sent) sm100::mbar_wait(&full[(done + i) % C::S], ((done + i) / C::S) & 1, &none, nullptr, kLimit / 4);
+        fine = false;
+        break;
+      }
+    } else {
+      cp_wait<0>();
+      __syncwarp();
+    }
 
     // join the warps' slots: m, l and O of every row
     float* mine = reinterpret_cast<float*>(ring);  // [R][D]
@@ -313,6 +393,7 @@ __global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
         if (c == 0) *reinterpret_cast<float2*>(a.part_ml + (slot * R + row) * 2) = make_float2(mm, sum);
       }
     }
+    if constexpr (TMA) sm100::fence_proxy_async_smem();  // the sums stood where the next unit's stages go
     __syncthreads();
     pos += k1 - k0;
   }
@@ -323,7 +404,7 @@ __global__ void __launch_bounds__(kAThreads, 2) tree_kernel(TreeArgs a) {
   if (tid == 0) {
     int all = 0;
     for (int w = 0; w < kAWarps; ++w) all += okmask[w * 8];
-    a.header[2 + blockIdx.x] = all;
+    a.header[2 + blockIdx.x] = fine ? all : -1;
   }
 }
 
@@ -407,10 +488,12 @@ TreePlan tree_plan(int N, int B, int Hq, int Hkv) {
 
 template <typename T, int D, int RT>
 cudaError_t launch_narrow(TreeArgs& a, int ctas, cudaStream_t s) {
-  auto kern = tree_kernel<T, D, RT>;
+  CUtensorMap mk{}, mv{};
+  tree_boxes(a, D, 16, &mk, &mv);
+  auto kern = a.box ? tree_kernel<T, D, RT, true> : tree_kernel<T, D, RT, false>;
   cudaError_t err = set_smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(tree_smem<D, RT>(kMaxBatch)));
   if (err != cudaSuccess) return err;
-  return launch_kernel(kern, dim3(ctas), dim3(kAThreads), tree_smem<D, RT>(a.B), s, true, a);
+  return launch_kernel(kern, dim3(ctas), dim3(kAThreads), tree_smem<D, RT>(a.B), s, true, a, mk, mv);
 }
 
 template <typename T>

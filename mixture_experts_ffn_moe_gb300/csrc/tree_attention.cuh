@@ -137,6 +137,16 @@ __device__ __forceinline__ Piece piece_at(const TreeArgs& a, const long long* pr
   return u;
 }
 
+// Tensor maps of the caches with boxes of a.box slots: the longest run, up to `most`, that lies in one page and stands
+// on 8-row groups of the swizzled tile.  a.box = 0 where there is none (or the strides do not fit a tensor map).
+inline void tree_boxes(TreeArgs& a, int D, int most, CUtensorMap* mk, CUtensorMap* mv) {
+  a.box = most;
+  while (a.box > 1 && a.page.d % a.box) a.box /= 2;
+  if (a.box < 8 || !encode_tmap_cache(mk, a.kc, D, a.page.d, a.Hkv, a.pages, a.k_slot, a.k_head, a.k_page, 64, a.box) ||
+      !encode_tmap_cache(mv, a.vc, D, a.page.d, a.Hkv, a.pages, a.v_slot, a.v_head, a.v_page, 64, a.box))
+    a.box = 0;
+}
+
 // Launches the tcgen05 kernel (tree_attention_wide.cu) on `ctas` CTAs, one an SM.
 cudaError_t launch_tree_wide(const TreeArgs& a, bool bf16, int D, int ctas, cudaStream_t s);
 

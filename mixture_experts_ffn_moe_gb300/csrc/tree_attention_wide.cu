@@ -529,12 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename T, int D>
 cudaError_t launch(TreeArgs a, int ctas, cudaStream_t s) {
   CUtensorMap mk{}, mv{};
-  // runs of slots that lie in one page and stand on 8-row groups of the swizzled tile
-  a.box = 128;
-  while (a.box > 1 && a.page.d % a.box) a.box /= 2;
-  if (a.box < 8 || !encode_tmap_cache(&mk, a.kc, D, a.page.d, a.Hkv, a.pages, a.k_slot, a.k_head, a.k_page, 64, a.box) ||
-      !encode_tmap_cache(&mv, a.vc, D, a.page.d, a.Hkv, a.pages, a.v_slot, a.v_head, a.v_page, 64, a.box))
-    a.box = 0;
+  tree_boxes(a, D, 128, &mk, &mv);
   auto kern = a.box ? tree_wide_kernel<T, D, true> : tree_wide_kernel<T, D, false>;
   cudaError_t err = set_smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(wide_smem<D>(kMaxBatch)));
   if (err != cudaSuccess) return err;
