@@ -42,7 +42,7 @@ template <int D> struct TreeCfg {
 
 template <int D, int RT> constexpr size_t tree_smem(int B) {
   return static_cast<size_t>(kAWarps) * (TreeCfg<D>::kRing > RT * 16 * D * 4 ? TreeCfg<D>::kRing : RT * 16 * D * 4) +
-         RT * 16 * D * 2 + (B + 1 + kAWarps) * 8 + kAWarps * (8 * 4 + 8 * 8 + RT * 16 * 8) + 16 + 1024;
+         RT * 16 * D * 2 + (2 * B + 1 + kAWarps) * 8 + kAWarps * (8 * 4 + 8 * 8 + RT * 16 * 8) + 16 + 1024;
 }
 
 constexpr long long kLimit = 4000000000LL;  // about 2 s of SM clocks a wait
@@ -58,8 +58,9 @@ __global__ void __launch_bounds__(kAThreads, 2)
   unsigned char* ring = smem + (threadIdx.x >> 5) * kWarpBytes;
   unsigned char* qs = smem + kAWarps * kWarpBytes;                                       // [R][D]
   long long* prefix = reinterpret_cast<long long*>(qs + R * D * 2);                      // [B + 1], then scan scratch
-  uint64_t* full = reinterpret_cast<uint64_t*>(prefix + a.B + 1 + kAWarps) + (threadIdx.x >> 5) * 8;  // [S] a warp (TMA)
-  float* ml = reinterpret_cast<float*>(prefix + a.B + 1 + kAWarps + kAWarps * 8);        // [warps][R][2]
+  int2* sizes = reinterpret_cast<int2*>(prefix + a.B + 1 + kAWarps);                     // [B]
+  uint64_t* full = reinterpret_cast<uint64_t*>(sizes + a.B) + (threadIdx.x >> 5) * 8;    // [S] a warp (TMA)
+  float* ml = reinterpret_cast<float*>(reinterpret_cast<uint64_t*>(sizes + a.B) + kAWarps * 8);  // [warps][R][2]
   uint32_t* okmask = reinterpret_cast<uint32_t*>(ml + kAWarps * R * 2) + (threadIdx.x >> 5) * 8;  // [S] a warp
   int* abort_s = reinterpret_cast<int*>(ml + kAWarps * R * 2) + kAWarps * 8;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(kAThreads, 2)
   }
   pdl_wait();
   int bad_plan;
-  plan_line<kAThreads>(a, prefix, prefix + a.B + 1, &bad_plan);
+  plan_line<kAThreads>(a, prefix, sizes, prefix + a.B + 1, &bad_plan);
   const long long total = prefix[a.B];
   const long long chunk = (total + gridDim.x - 1) / gridDim.x;
   if (blockIdx.x == 0) {
@@ -91,7 +92,9 @@ __global__ void __launch_bounds__(kAThreads, 2)
   long long pos = blockIdx.x * chunk;
   const long long end = pos + chunk < total ? pos + chunk : total;
   while (pos < end) {
-    const Piece u = piece_at(a, prefix, pos, end, 0);
+    const Piece u = piece_at(a, prefix, sizes, pos, end, 0);
+    pos += u.places;
+    if (u.rows == 0) continue;
     const int b = u.b, ctx = u.ctx, L = u.ctx + u.n, kt = u.kt, k0 = u.k0, k1 = u.k1, head = u.head, row0 = u.row0;
     const int rows = u.rows, node0 = u.node0;
     const T* kbase = static_cast<const T*>(a.kc) + head * a.k_head;
@@ -395,7 +398,6 @@ __global__ void __launch_bounds__(kAThreads, 2)
     }
     if constexpr (TMA) sm100::fence_proxy_async_smem();  // the sums stood where the next unit's stages go
     __syncthreads();
-    pos += k1 - k0;
   }
   bad_pages = __reduce_add_sync(0xffffffffu, bad_pages);
   __syncthreads();
@@ -431,13 +433,13 @@ __global__ void __launch_bounds__(128) tree_join_kernel(TreeArgs a) {
   const int group = a.group.d, head = hq / group, r = j * group + (hq - head * group);
   const int kt = (ctx + n + a.tile - 1) / a.tile, per = a.rows * a.ranks, rt_n = (n * group + per - 1) / per;
   const long long chunk = a.prefix[a.B + 1];
-  const long long s = a.prefix[b] + (static_cast<long long>(head) * rt_n + r / per) * kt, e = s + kt;
-  const long long c0 = s / chunk, c1 = (e - 1) / chunk;
+  const long long s = a.prefix[b] + (static_cast<long long>(head) * rt_n + r / per) * (kt + a.setup), e = s + a.setup + kt;
+  const long long c0 = (s + a.setup) / chunk, c1 = (e - 1) / chunk;  // from the CTA with the unit's first tile
   if (c0 == c1) return;
   const int rank = r % per / a.rows, row = r % a.rows, parts = static_cast<int>(c1 - c0 + 1);
   auto at = [&](int p) {
     const long long c = c0 + p;
-    return ((c * a.ranks + rank) * 2 + (c * chunk > s ? 0 : 1)) * a.rows + row;
+    return ((c * a.ranks + rank) * 2 + (p == 0 ? 1 : 0)) * a.rows + row;
   };
   float mm = -INFINITY;
   for (int p = lane; p < parts; p += 32) mm = fmaxf(mm, a.part_ml[at(p) * 2]);
@@ -584,6 +586,7 @@ extern "C" moe_status_t moe_tree_attention(const moe_tree_attention_args_t* r, v
     a.tile = p.wide ? kWideTile : kTile;
     a.rows = p.rows;
     a.ranks = p.ranks;
+    a.setup = p.wide ? 2 : 3;
     const bool one_tile = static_cast<long long>(r->table_width) * r->page_size <= a.tile;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return launched("moe_tree_attention", r->dtype == MOE_DTYPE_FP16 ? launch_tree<__half>(a, r->dim, p, sms, one_tile, s)

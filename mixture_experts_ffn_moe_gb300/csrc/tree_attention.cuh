@@ -27,12 +27,13 @@ struct TreeArgs {
   long long table_ld;
   int N, B, Hq, Hkv, pages, table_w;
   int tile, rows, ranks;  // slots of a tile, rows of a CTA's row tile, CTAs that work on one range side by side
+  int setup;              // places on the line before a unit's first tile: what starting one costs, in tiles
   FastDiv page, group;
   int box;                // slots of a page that one TMA copy brings (0: cp.async)
   float scale_log2;
   int32_t* header;    // workspace: [0] CTAs, [1] bad lengths, offsets or counts, then for every CTA its bad pages
                       // (negative: one of its waits gave up)
-  long long* prefix;  // [B + 1] first tile of every sequence on the line, [B + 1] = tiles a group of CTAs
+  long long* prefix;  // [B + 1] first place of every sequence on the line, [B + 1] = places a group of CTAs
   float* part_o;      // [CTAs * 2][rows][D]
   float* part_ml;     // [CTAs * 2][rows][2]
 };
@@ -70,9 +71,10 @@ __device__ __forceinline__ void seq_sizes(const TreeArgs& a, int b, int& ctx, in
   if (ctx > room - n) { ctx = static_cast<int>(room - n); bad = 1; }
 }
 
-// prefix[b] = first tile of sequence b on the line of all tiles.
+// prefix[b] = first place of sequence b on the line: `setup` places and its tiles for every unit.  sizes[b] = (committed
+// slots, nodes).
 template <int THREADS>
-__device__ __forceinline__ void plan_line(const TreeArgs& a, long long* prefix, long long* scratch, int* bad) {
+__device__ __forceinline__ void plan_line(const TreeArgs& a, long long* prefix, int2* sizes, long long* scratch, int* bad) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long base = 0;
   int nbad = 0;
@@ -83,9 +85,10 @@ __device__ __forceinline__ void plan_line(const TreeArgs& a, long long* prefix, 
       int ctx, n, bd;
       seq_sizes(a, b, ctx, n, bd);
       nbad += bd;
+      sizes[b] = make_int2(ctx, n);
       if (n > 0) {
         const int per = a.rows * a.ranks, rt = (n * static_cast<int>(a.group.d) + per - 1) / per;
-        tiles = static_cast<long long>(a.Hkv) * rt * ((static_cast<long long>(ctx) + n + a.tile - 1) / a.tile);
+        tiles = static_cast<long long>(a.Hkv) * rt * (a.setup + (static_cast<long long>(ctx) + n + a.tile - 1) / a.tile);
       }
     }
     long long incl = tiles;
@@ -110,11 +113,14 @@ __device__ __forceinline__ void plan_line(const TreeArgs& a, long long* prefix, 
   __syncthreads();
 }
 
-// A CTA group's piece of one unit: sequence, KV head, row tile, and the tiles [k0, k1) of the unit's kt.
+// A CTA group's piece of one unit: sequence, KV head, row tile, and the tiles [k0, k1) of the unit's kt (none where the
+// piece ends within the unit's setup); `places` is its length on the line.
 struct Piece {
   int b, ctx, n, head, row0, rows, node0, k0, k1, kt;
+  long long places;
 };
-__device__ __forceinline__ Piece piece_at(const TreeArgs& a, const long long* prefix, long long pos, long long end, int rank) {
+__device__ __forceinline__ Piece piece_at(const TreeArgs& a, const long long* prefix, const int2* sizes, long long pos, long long end,
+                                          int rank) {
   Piece u;
   int lo = 0, hi = a.B;  // prefix[lo] <= pos < prefix[hi]
   while (hi - lo > 1) {
@@ -122,17 +128,19 @@ __device__ __forceinline__ Piece piece_at(const TreeArgs& a, const long long* pr
     if (prefix[mid] <= pos) lo = mid; else hi = mid;
   }
   u.b = lo;
-  int bad;
-  seq_sizes(a, u.b, u.ctx, u.n, bad);
+  u.ctx = sizes[u.b].x;
+  u.n = sizes[u.b].y;
   u.kt = (u.ctx + u.n + a.tile - 1) / a.tile;
+  const int span = u.kt + a.setup;
   const int group = a.group.d, per = a.rows * a.ranks, rt_n = (u.n * group + per - 1) / per;
   const long long rel = pos - prefix[u.b];
-  const int unit = static_cast<int>(rel / u.kt);
-  u.k0 = static_cast<int>(rel - static_cast<long long>(unit) * u.kt);
-  u.k1 = static_cast<int>(end - pos < u.kt - u.k0 ? u.k0 + (end - pos) : u.kt);
+  const int unit = static_cast<int>(rel / span), p0 = static_cast<int>(rel - static_cast<long long>(unit) * span);
+  u.places = min(end - pos, static_cast<long long>(span - p0));
+  u.k0 = max(0, p0 - a.setup);
+  u.k1 = max(0, p0 + static_cast<int>(u.places) - a.setup);
   u.head = unit / rt_n;
   u.row0 = (unit - u.head * rt_n) * per + rank * a.rows;
-  u.rows = max(0, min(a.rows, u.n * group - u.row0));
+  u.rows = u.k1 > u.k0 ? max(0, min(a.rows, u.n * group - u.row0)) : 0;  // no rows: nothing to do
   u.node0 = a.offs[u.b];
   return u;
 }

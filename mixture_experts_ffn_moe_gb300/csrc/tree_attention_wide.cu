@@ -37,7 +37,7 @@ template <int D> struct WideCfg {
   static constexpr int kData = (2 + 2 * NS) * kTileBytes;
   static constexpr int kSmall = 1024;                  // barriers, masks, marks
 };
-template <int D> size_t wide_smem(int B) { return 1024 + WideCfg<D>::kData + WideCfg<D>::kSmall + (static_cast<size_t>(B) + 1 + kThreads / 32) * 8; }
+template <int D> size_t wide_smem(int B) { return 1024 + WideCfg<D>::kData + WideCfg<D>::kSmall + (2 * static_cast<size_t>(B) + 1 + kThreads / 32) * 8; }
 
 struct Small {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   unsigned char* vs = ks + C::NS * C::kTileBytes;             // [NS]
   Small& sm = *reinterpret_cast<Small*>(base + C::kData);
   long long* prefix = reinterpret_cast<long long*>(base + C::kData + C::kSmall);
+  int2* sizes = reinterpret_cast<int2*>(prefix + a.B + 1 + kThreads / 32);  // [B]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
 
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 12) tmem_alloc(&sm.tmem, 512);
   pdl_wait();
   int bad_plan;
-  plan_line<kThreads>(a, prefix, prefix + a.B + 1, &bad_plan);  // (its barriers also publish the set-up above)
+  plan_line<kThreads>(a, prefix, sizes, prefix + a.B + 1, &bad_plan);  // (its barriers also publish the set-up above)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -164,8 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t s_tm = tmem + lanes + i * 128, o_tm = tmem + lanes + 256 + i * D;
     int n = 0, piece = 0, done = 0;  // tiles of the CTA, pieces, tiles of this half
     for (long long pos = first; pos < end;) {
-      const Piece u = piece_at(a, prefix, pos, end, rank);
-      pos += u.k1 - u.k0;
+      const Piece u = piece_at(a, prefix, sizes, pos, end, rank);
+      pos += u.places;
       if (u.rows == 0) continue;
       const int row = i * 128 + r_in;
       const bool mine = i == 0 || u.rows > 128;  // has this half any row?
@@ -340,8 +341,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool fine = true;
         const int boxes = 128 / a.box;
         for (long long pos = first; pos < end && fine;) {
-          const Piece u = piece_at(a, prefix, pos, end, rank);
-          pos += u.k1 - u.k0;
+          const Piece u = piece_at(a, prefix, sizes, pos, end, rank);
+          pos += u.places;
           if (u.rows == 0) continue;
           const int32_t* table = a.table + u.b * a.table_ld;
           const int L = u.ctx + u.n;
@@ -397,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(q & 1 ? &sm.v_full[t % C::NS] : &sm.k_full[t % C::NS]);
     };
     for (long long pos = first; pos < end && fine;) {
-      const Piece u = piece_at(a, prefix, pos, end, rank);
-      pos += u.k1 - u.k0;
+      const Piece u = piece_at(a, prefix, sizes, pos, end, rank);
+      pos += u.places;
       if (u.rows == 0) continue;
       const int32_t* table = a.table + u.b * a.table_ld;
       const T* kbase = static_cast<const T*>(a.kc) + u.head * a.k_head;
@@ -473,8 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&sm.s_full[i]);
       };
       for (long long pos = first; pos < end && fine;) {
-        const Piece u = piece_at(a, prefix, pos, end, rank);
-        pos += u.k1 - u.k0;
+        const Piece u = piece_at(a, prefix, sizes, pos, end, rank);
+        pos += u.places;
         if (u.rows == 0) continue;
         const int nq = u.rows > 128 ? 2 : 1, T0 = n, T1 = n + (u.k1 - u.k0);
         fine = wait(&sm.q_full, piece & 1) && wait(&sm.k_full[n % C::NS], (n / C::NS) & 1);
