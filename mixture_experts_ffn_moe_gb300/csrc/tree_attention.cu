@@ -586,7 +586,7 @@ extern "C" moe_status_t moe_tree_attention(const moe_tree_attention_args_t* r, v
     a.tile = p.wide ? kWideTile : kTile;
     a.rows = p.rows;
     a.ranks = p.ranks;
-    a.setup = p.wide ? 2 : 3;
+    a.setup = 4;  // measured 2, 3, 4, 6, 9: 56.3, 53.3, 53.4, 53.9, 56.1 us for ragged short units, 478 to 467 us for long ones
     const bool one_tile = static_cast<long long>(r->table_width) * r->page_size <= a.tile;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return launched("moe_tree_attention", r->dtype == MOE_DTYPE_FP16 ? launch_tree<__half>(a, r->dim, p, sms, one_tile, s)
