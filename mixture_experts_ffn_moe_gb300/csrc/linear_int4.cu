@@ -37,6 +37,8 @@ namespace {
 constexpr int kKBlock = 128;
 constexpr size_t kLinearSmem = 224 * 1024;
 
+template <int N> constexpr int kLog2 = 1 + kLog2<N / 2>;
+template <> constexpr int kLog2<1> = 0;
 template <int RT> constexpr int kInFlight = RT == 1 ? 4 : 2;  // blocks in flight a warp: 128 bytes a lane
 
 template <int G> struct Lanes;  // a lane's codes of a block: 4 / P words in each of P phases (one a group)
@@ -55,41 +57,45 @@ template <int G, int RT> struct Block {
   float s[RT][2];  // of group t of the block (t < P), shared in the quad
 };
 
-// One piece: 8 values of x by one of the 16 neighbouring threads of a block and token (c = 0..15, all 16 take part):
-// the values in their frame and order, the group's sum as stored, the block's factor, and whether all is finite.
+// One piece: 8 values of x by one of the 16 neighbouring threads of a block and token (all 16 take part): the values in
+// their frame and order, and the frame's factor.
 struct PieceOfX {
   uint4 h;
-  float sum, factor;
-  bool odd;
+  float factor;
 };
-template <int G>
 __device__ __forceinline__ PieceOfX make_piece(uint4 v, bool bf16) {
+  // magnitudes of either type are ordered like their bit patterns: the largest of the block, two at a time
+  uint32_t top = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+  top = max(top & 0xffffu, top >> 16);
+  const int fe = x_frame_exp(bf16 ? Elem<__nv_bfloat16>::unpack(top).x : Elem<__half>::unpack(top).x);
+  const float mul = exp2i(-fe), low = mul * 0.0625f;
   const uint32_t e[4] = {v.x, v.y, v.z, v.w};
-  float f[8], top = 0.f;
+  float f[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float2 q = bf16 ? Elem<__nv_bfloat16>::unpack(e[j]) : Elem<__half>::unpack(e[j]);
     f[2 * j] = q.x;
     f[2 * j + 1] = q.y;
-    top = fmaxf(top, fmaxf(fabsf(q.x), fabsf(q.y)));
   }
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const int fe = x_frame_exp(top);
-  const float mul = exp2i(-fe), low = mul * 0.0625f;
   PieceOfX r;
   // (k0,k4) (k1,k5)/16 (k2,k6) (k3,k7)/16
   r.h = make_uint4(pack_half2(f[0] * mul, f[4] * mul), pack_half2(f[1] * low, f[5] * low),
                    pack_half2(f[2] * mul, f[6] * mul), pack_half2(f[3] * low, f[7] * low));
-  const float2 s0 = Elem<__half>::unpack(r.h.x), s1 = Elem<__half>::unpack(r.h.y), s2 = Elem<__half>::unpack(r.h.z), s3 = Elem<__half>::unpack(r.h.w);
+  r.factor = exp2i(fe + 12);
+  return r;
+}
+// The sum of a group's values of one token (its G / 8 neighbouring threads' pieces), in the frame.
+template <int G>
+__device__ __forceinline__ float sum_of_group(uint4 h) {
+  const float2 s0 = Elem<__half>::unpack(h.x), s1 = Elem<__half>::unpack(h.y), s2 = Elem<__half>::unpack(h.z), s3 = Elem<__half>::unpack(h.w);
   float sum = (s0.x + s0.y) + (s2.x + s2.y) + 16.f * ((s1.x + s1.y) + (s3.x + s3.y));
 #pragma unroll
   for (int o = 1; o < G / 8; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  r.sum = sum * (-8.f * 0x1p-24f);
-  r.factor = exp2i(fe + 12);
-  r.odd = !(fabsf(sum) < INFINITY);
-  return r;
+  return sum;
 }
+constexpr float kMinusBias = -8.f * 0x1p-24f;  // of a code, in the units of the products
 
 // The weight stream of a warp: its blocks of every tile of the CTA, in order.
 template <int G, int RT, int NW> struct Stream {
@@ -107,19 +113,19 @@ template <int G, int RT, int NW> struct Stream {
   __device__ __forceinline__ Stream(const LinearArgs& args, int warp, int lane) : a(args) {
     gated = RT == 2 && a.gated;
     const int RW = gated ? 16 : RT * 16;
-    wk = NW / a.wr;
-    const int wrow = warp / wk;
-    wkid = warp - wrow * wk;
+    wk = 1 << a.wk_log2;
+    const int wrow = warp >> a.wk_log2;
+    wkid = warp & (wk - 1);
     wrow_base = wrow * RW;
     lane_row = lane >> 2;
     kbytes = a.K >> 1;
     nblk = (a.K + kKBlock - 1) / kKBlock;
     full = a.K / kKBlock;
     groups = a.K / G;
-    tile_rows = RW * a.wr;
-    tiles = (a.N + tile_rows - 1) / tile_rows;
-    rem = nblk % wk;
-    rounds = ((nblk + wk - 1) / wk + kInFlight<RT> - 1) / kInFlight<RT> * kInFlight<RT>;  // some may be empty
+    tile_rows = RW << (kLog2<NW> - a.wk_log2);
+    tiles = a.tiles;
+    rem = nblk & (wk - 1);
+    rounds = (((nblk + wk - 1) >> a.wk_log2) + kInFlight<RT> - 1) / kInFlight<RT> * kInFlight<RT>;  // some may be empty
     up_w = gated ? static_cast<long long>(a.N) * kbytes : 0;
     up_s = gated ? static_cast<long long>(a.N) * groups : 0;
     tile = blockIdx.x;
@@ -127,7 +133,7 @@ template <int G, int RT, int NW> struct Stream {
     enter(lane & 3);
   }
   // first block of the warp in the CTA's it-th tile: the longer shares go round
-  __device__ __forceinline__ int start(int i) const { return (wkid + i * rem) % wk; }
+  __device__ __forceinline__ int start(int i) const { return (wkid + i * rem) & (wk - 1); }
   __device__ __forceinline__ void enter(int t) {
     const long long first = min(tile * tile_rows + wrow_base, a.N - 1);
     wbase = a.w + first * kbytes;
@@ -301,35 +307,56 @@ __global__ void __launch_bounds__(NW * 32, 1) linear_int4_kernel(LinearArgs a) {
   float* sums = reinterpret_cast<float*>(xf + nblk * 128);
   pdl_trigger();
   if (tid == 0) odd = 0;
-  pdl_wait();
   Stream<G, RT, NW> st(a, warp, lane);
-  Block<G, RT> buf[U];
-#pragma unroll
-  for (int u = 0; u < U; ++u) st.fetch(buf[u], t);
-  __syncthreads();
+  pdl_wait();
 
-  // tokens past the last one are left as they are: columns of a product do not mix
-  constexpr int B = 7;  // loads in flight a thread
+  // x: 16 neighbouring threads a block and token.  Tokens past the last one are left as they are: columns of a product
+  // do not mix.  The first loads of x and of the weights are under way together.
+  constexpr int B = 4;  // loads in flight a thread
   const int pieces = nblk * a.M * 16;
-  for (int w0 = warp * 32; w0 < pieces; w0 += B * NW * 32) {  // whole warps: the threads of a piece talk to each other
-    uint4 v[B];
+  uint4 v[B];
+  auto load_x = [&](int w0) {
 #pragma unroll
     for (int k = 0; k < B; ++k) {
-      const int i = w0 + lane + k * NW * 32, bm = i >> 4, b = bm / a.M, m = bm - b * a.M, col = b * kKBlock + (i & 15) * 8;
+      const int i = w0 + lane + k * NW * 32, b = div_by(i >> 4, a.tokens_div), m = (i >> 4) - b * a.M, col = b * kKBlock + (i & 15) * 8;
       v[k] = make_uint4(0, 0, 0, 0);
       if (i < pieces && col < a.K) v[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ldx + col);
     }
+  };
+  load_x(warp * 32);
+  Block<G, RT> buf[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) st.fetch(buf[u], t);
+  for (int w0 = warp * 32; w0 < pieces; w0 += B * NW * 32) {  // whole warps: the threads of a piece talk to each other
+    if (w0 != warp * 32) load_x(w0);
 #pragma unroll
     for (int k = 0; k < B; ++k) {
-      const int i = w0 + lane + k * NW * 32, bm = i >> 4, b = bm / a.M, m = bm - b * a.M;
+      const int i = w0 + lane + k * NW * 32, b = div_by(i >> 4, a.tokens_div), m = (i >> 4) - b * a.M;
       if (w0 + k * NW * 32 >= pieces) break;
-      const PieceOfX x = make_piece<G>(v[k], a.bf16);
+      const PieceOfX x = make_piece(v[k], a.bf16);
       if (i < pieces) {
         const int c = i & 15, p = c / (G / 8), cp = c % (G / 8);
         xf[b * 128 + (p * (4 / P) + cp % (G / 32)) * 32 + m * 4 + cp / (G / 32)] = x.h;
-        if (cp == 0) sums[(b * (P + 1) + p) * 8 + m] = x.sum;
         if (c == 0) sums[(b * (P + 1) + P) * 8 + m] = x.factor;
-        if (x.odd) odd = 1;
+      }
+    }
+  }
+  __syncthreads();
+  // the groups' sums: products with rows of ones (16 where the pieces stand divided by 16)
+  for (int b = warp; b < nblk; b += NW) {
+    const uint32_t ones[4] = {0x3c003c00u, 0x3c003c00u, 0x4c004c00u, 0x4c004c00u};
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < 4 / P; ++j) {
+        const uint4 x = xf[b * 128 + (p * (4 / P) + j) * 32 + lane];
+        mma_f16_16816(d, ones, x.x, x.y);
+        mma_f16_16816(d, ones, x.z, x.w);
+      }
+      if (lane < 4) {  // row 0, tokens 2t and 2t + 1
+        *reinterpret_cast<float2*>(sums + (b * (P + 1) + p) * 8 + 2 * t) = make_float2(d[0] * kMinusBias, d[1] * kMinusBias);
+        if ((2 * t < a.M && !(fabsf(d[0]) < INFINITY)) || (2 * t + 1 < a.M && !(fabsf(d[1]) < INFINITY))) odd = 1;
       }
     }
   }
@@ -367,15 +394,16 @@ __global__ void __launch_bounds__(256) linear_pieces_kernel(LinearArgs a) {
   const int b = blockIdx.x, c = threadIdx.x & 15, col = b * kKBlock + c * 8, m = blockIdx.y * 16 + (threadIdx.x >> 4);
   uint4 v = make_uint4(0, 0, 0, 0);
   if (m < a.M && col < a.K) v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ldx + col);
-  const PieceOfX x = make_piece<G>(v, a.bf16);
+  const PieceOfX x = make_piece(v, a.bf16);
+  const float sum = sum_of_group<G>(x.h);
   const int part = m / a.mt, mp = m - part * a.mt;
   float* sums = a.sums + (static_cast<long long>(b) * (a.tokens / a.mt) + part) * ((P + 1) * a.mt + 4);
   if (m < a.M) {
     a.xf[static_cast<long long>(m) * gridDim.x * 16 + b * 16 + c] = x.h;
-    if (c % (G / 8) == 0) sums[c / (G / 8) * a.mt + mp] = x.sum;
+    if (c % (G / 8) == 0) sums[c / (G / 8) * a.mt + mp] = sum * kMinusBias;
     if (c == 0) sums[P * a.mt + mp] = x.factor;
   }
-  const bool odd = __syncthreads_or(x.odd && m < a.M);
+  const bool odd = __syncthreads_or(!(fabsf(sum) < INFINITY) && m < a.M);
   if (threadIdx.x == 0) {
     sums[(P + 1) * a.mt + mp / 16] = odd ? 1.f : 0.f;
     if (b == 0 && blockIdx.y == 0) *a.status = DeviceStatus{};
@@ -402,13 +430,16 @@ template <int G, int RT>
 cudaError_t launch_resident(LinearArgs a, int sms, cudaStream_t s) {
   constexpr int NW = 16;
   const int RW = a.gated ? 16 : RT * 16, nblk = (a.K + kKBlock - 1) / kKBlock;
-  a.wr = choose_wr(a, RW, NW, sms);
-  const int tiles = (a.N + RW * a.wr - 1) / (RW * a.wr);
+  const int wr = choose_wr(a, RW, NW, sms);
+  a.wk_log2 = 0;
+  while ((wr << a.wk_log2) < NW) ++a.wk_log2;
+  a.tiles = (a.N + RW * wr - 1) / (RW * wr);
+  a.tokens_div = fast_div(a.M);
   auto kern = linear_int4_kernel<G, RT, NW>;
   cudaError_t err = set_smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(kLinearSmem));
   if (err != cudaSuccess) return err;
   const size_t smem = NW * 8 * (RT * 16 + 4) * 4 + static_cast<size_t>(nblk) * (2048 + (Lanes<G>::P + 1) * 32);
-  return launch_kernel(kern, dim3(tiles < sms ? tiles : sms), dim3(NW * 32), smem, s, true, a);
+  return launch_kernel(kern, dim3(a.tiles < sms ? a.tiles : sms), dim3(NW * 32), smem, s, true, a);
 }
 
 template <int G>

@@ -13,7 +13,9 @@ struct LinearArgs {
   void* y;             // [M, N], row stride ldy
   long long ldx, ldy;
   int M, N, K, gated, bf16;
-  int wr;              // warps that share a tile's blocks in the row direction (the others split K)
+  // up to 8 rows: warps that split the K of a tile (log2; the others take other rows), tiles
+  int wk_log2, tiles;
+  FastDiv tokens_div;
   // more than 8 rows (workspace): x as the products take it
   int tokens;          // M rounded up to whole products
   uint4* xf;           // fp16 [tokens][blocks * 128], each 8 columns in the codes' order
