@@ -1,8 +1,10 @@
 """Builds libgbmoe.so (the C-ABI CUDA library) in-tree for sm_103a.
 
 Each .cu file is compiled by its own nvcc process (in parallel), then the
-objects are linked into a shared library next to this file.  Nothing is
-installed anywhere else.
+objects are linked into a shared library next to this file.  The C++ binding of
+the decode-step operators (csrc/step_bindings.cpp, against the installed torch's
+headers) is compiled beside them into _step_bindings.so.  Nothing is installed
+anywhere else.
 
     python -m mixture_experts_ffn_moe_gb300.build [--verbose]
 """
@@ -21,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgbmoe.so")
+STEPS = os.path.join(PKG, "_step_bindings.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -47,22 +50,46 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_steps() -> None:
+    """The Python binding of the decode-step operators, with the host compiler."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    includes = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], cuda]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE]
+    for path in includes:
+        cmd += ["-isystem", path]
+    cmd += [os.path.join(CSRC, "step_bindings.cpp"), "-o", STEPS + ".tmp", "-L", os.path.join(root, "lib"), "-lc10",
+            "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"the host compiler failed on step_bindings.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(STEPS + ".tmp", STEPS)
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(STEPS):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(STEPS))
     deps = glob.glob(os.path.join(CSRC, "*")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
     return any(os.path.getmtime(p) > t for p in deps)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libgbmoe.so if a source is newer than it; returns its path."""
+    """Compile and link libgbmoe.so and _step_bindings.so if a source is newer; returns the library's path."""
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        steps = ex.submit(_compile_steps)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        steps.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), "-shared", "-o", tmp] + objs + ARCH
     r = subprocess.run(cmd, capture_output=True, text=True)

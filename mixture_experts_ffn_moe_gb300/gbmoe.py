@@ -2,15 +2,15 @@
 
 Argument marshalling only: every step of the layer runs in the library's
 CUDA kernels.  torch supplies device memory and the current CUDA stream.
-There is no fallback: if the library is missing, every call raises.
+There is no fallback: if the library is missing, every call raises.  The short
+calls of a decode step around the layer are marshalled in C++ (_step_bindings).
 """
 from __future__ import annotations
 
 import ctypes
-import functools
+import importlib.util
 import math
 import os
-import struct
 
 import torch
 
@@ -443,45 +443,26 @@ def moe_profile_read(max_stages: int = 8):
 
 
 # ------------------------------------------------------------------ operators of a decode step around the layer
-# The argument structs are packed by `struct` (native sizes and alignment, as the C compiler lays them out).
-_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_FP16, torch.float32: MOE_DTYPE_FP32}
-_ROPE_ARGS = struct.Struct("@9if2i3P3P3P6q5q3q")
-_TREE_ARGS = struct.Struct("@9ifq3P3PPP4q6q")
+# Their tensors are checked and their arguments filled in by _step_bindings.so (csrc/step_bindings.cpp): marshalling
+# calls this short in Python took longer than the calls.  It is built beside the library and given its entry points.
+STEPS_PATH = os.path.join(_PKG, "_step_bindings.so")
+_steps = None
 
 
-# A decode step makes many short calls, so the bindings test their arguments in one expression and look for the
-# reason only where it fails.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-def _fail_tensor(t, device, dtype, shape, name, contiguous):
-    """Raises ValueError if `t` is not a CUDA tensor of this device, type and shape (None: any size)."""
-    if t.get_device() < 0 or t.get_device() != device:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the other tensors")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
-        raise ValueError(f"{name} has the shape {list(t.shape)}, expected {['any' if w is None else w for w in shape]}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if not contiguous and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-
-
-def _fail(device, *checks):
-    """Raises the first error of (tensor, dtype, shape, name, contiguous) checks."""
-    for t, dtype, shape, name, contiguous in checks:
-        _fail_tensor(t, device, dtype, shape, name, contiguous)
-    raise ValueError("inconsistent arguments")
-
-
-def _float_dtype(t: torch.Tensor, name: str, allowed) -> int:
-    d = _DTYPES.get(t.dtype)
-    if d is None or d not in allowed:
-        raise ValueError(f"{name} has an unsupported type {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return d
+def _load_steps():
+    global _steps
+    if _steps is None:
+        lib = load()
+        if not os.path.exists(STEPS_PATH):
+            raise RuntimeError(f"{STEPS_PATH} is missing: build it with `python -m mixture_experts_ffn_moe_gb300.build`")
+        spec = importlib.util.spec_from_file_location("_step_bindings", STEPS_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.moe_rope, lib.moe_linear_int4, lib.moe_linear_int4_workspace_size, lib.moe_tree_attention,
+            lib.moe_tree_attention_workspace_size, lib.moe_verify_draft)))
+        _steps = module
+    return _steps
 
 
 def rope_frequencies(rot_dim, base=10000.0, scaling="none", factor=1.0, original_positions=0, beta_fast=32.0,
@@ -528,41 +509,10 @@ def moe_rope(q, k, positions, inv_freq, scale=1.0, interleaved=False, inverse=Fa
     The 2 * len(inv_freq) elements from `offset` on turn by position * inv_freq; the rest is copied.  q_out and
     k_out may be the inputs (in place).  See include/gbmoe.h.
     """
-    dtype = q.dtype
-    dt = _float_dtype(q, "q", (0, 1, 2))
-    dev = q.get_device()
-    if q.dim() != 3:
-        raise ValueError("q must be [tokens, heads, dim]")
-    T, hq, D = q.shape
-    if q_out is None:
-        q_out = torch.empty((T, hq, D), dtype=dtype, device=q.device)
-    qt, qh, qd = q.stride()
-    ot, oh, od = q_out.stride()
-    if not ((qd == 1 or D == 1) and (od == 1 or D == 1) and q_out.dtype is dtype and q_out.get_device() == dev
-            and q_out.shape == q.shape and positions.dtype is torch.int32 and positions.get_device() == dev
-            and positions.shape == (T,) and positions.is_contiguous() and inv_freq.dtype is torch.float64
-            and inv_freq.get_device() == dev and inv_freq.dim() == 1 and inv_freq.is_contiguous()):
-        _fail(dev, (q, dtype, (T, hq, D), "q", False), (q_out, dtype, (T, hq, D), "q_out", False),
-              (positions, torch.int32, (T,), "positions", True), (inv_freq, torch.float64, (None,), "inv_freq", True))
-    hk = kp = kop = kt = kh = kot = koh = 0
-    if k is not None:
-        hk = k.shape[1] if k.dim() == 3 else 0
-        if k_out is None:
-            k_out = torch.empty((T, hk, D), dtype=dtype, device=q.device)
-        if not (k.dtype is dtype and k_out.dtype is dtype and k.get_device() == dev and k_out.get_device() == dev
-                and k.shape == (T, hk, D) and k_out.shape == (T, hk, D)
-                and (D == 1 or (k.stride(2) == 1 and k_out.stride(2) == 1))):
-            _fail(dev, (k, dtype, (T, None, D), "k", False), (k_out, dtype, (T, hk, D), "k_out", False))
-        kt, kh, _ = k.stride()
-        kot, koh, _ = k_out.stride()
-        kp, kop = k.data_ptr(), k_out.data_ptr()
-    args = _ROPE_ARGS.pack(dt, T, D, 2 * inv_freq.shape[0], offset, interleaved, inverse, hq, hk, scale, 0, 0,
-                           positions.data_ptr(), inv_freq.data_ptr(), 0, q.data_ptr(), kp, 0, q_out.data_ptr(), kop,
-                           0, qt, qh, kt, kh, 0, 0, ot, oh, 0, kot, koh, 0, 0, 0)
-    st = (_lib or load()).moe_rope(args, _raw_stream(dev))
-    if st:
-        _check(st, "moe_rope")
-    return q_out, k_out
+    r = (_steps or _load_steps()).rope(q, k, positions, inv_freq, scale, interleaved, inverse, offset, q_out, k_out)
+    if type(r) is int:
+        _check(r, "moe_rope")
+    return r
 
 
 def moe_rope_append(q, k, v, positions, inv_freq, slots, k_cache, v_cache, scale=1.0, interleaved=False,
@@ -572,54 +522,15 @@ def moe_rope_append(q, k, v, positions, inv_freq, slots, k_cache, v_cache, scale
     slots int32 [tokens]: page * page_size + row in k_cache / v_cache [pages, page_size, k_heads, dim]; entries
     outside the cache (such as -1) are skipped.
     """
-    dtype = q.dtype
-    dt = _float_dtype(q, "q", (0, 1, 2))
-    dev = q.get_device()
-    if q.dim() != 3 or k.dim() != 3 or k_cache.dim() != 4:
-        raise ValueError("q and k must be [tokens, heads, dim], k_cache [pages, page_size, k_heads, dim]")
-    T, hq, D = q.shape
-    hk = k.shape[1]
-    if q_out is None:
-        q_out = torch.empty((T, hq, D), dtype=dtype, device=q.device)
-    shape, cache = (T, hk, D), k_cache.shape
-    if not (k.shape == shape and v.shape == shape and q_out.shape == q.shape and cache == v_cache.shape
-            and cache[2] == hk and cache[3] == D and positions.shape == (T,) and slots.shape == (T,)
-            and k.dtype is dtype and v.dtype is dtype and q_out.dtype is dtype and k_cache.dtype is dtype
-            and v_cache.dtype is dtype and positions.dtype is torch.int32 and slots.dtype is torch.int32
-            and inv_freq.dtype is torch.float64 and inv_freq.dim() == 1 and k.get_device() == dev
-            and v.get_device() == dev and q_out.get_device() == dev and k_cache.get_device() == dev
-            and v_cache.get_device() == dev and positions.get_device() == dev and slots.get_device() == dev
-            and inv_freq.get_device() == dev and positions.is_contiguous() and slots.is_contiguous()
-            and inv_freq.is_contiguous()):
-        _fail(dev, (k, dtype, shape, "k", False), (v, dtype, shape, "v", False),
-              (q_out, dtype, (T, hq, D), "q_out", False), (k_cache, dtype, (None, None, hk, D), "k_cache", False),
-              (v_cache, dtype, tuple(cache), "v_cache", False), (positions, torch.int32, (T,), "positions", True),
-              (slots, torch.int32, (T,), "slots", True), (inv_freq, torch.float64, (None,), "inv_freq", True))
-    qt, qh, q1 = q.stride()
-    kt, kh, k1 = k.stride()
-    vt, vh, v1 = v.stride()
-    ot, oh, o1 = q_out.stride()
-    kcp, kcs, kch, kc1 = k_cache.stride()
-    vcp, vcs, vch, vc1 = v_cache.stride()
-    if D > 1 and not q1 == k1 == v1 == o1 == kc1 == vc1 == 1:
-        raise ValueError("the last dimension of every tensor must be contiguous")
-    args = _ROPE_ARGS.pack(dt, T, D, 2 * inv_freq.shape[0], offset, interleaved, inverse, hq, hk, scale, cache[1],
-                           cache[0], positions.data_ptr(), inv_freq.data_ptr(), slots.data_ptr(), q.data_ptr(),
-                           k.data_ptr(), v.data_ptr(), q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), qt,
-                           qh, kt, kh, vt, vh, ot, oh, kcp, kcs, kch, vcp, vcs, vch)
-    st = (_lib or load()).moe_rope(args, _raw_stream(dev))
-    if st:
-        _check(st, "moe_rope")
-    return q_out
+    r = (_steps or _load_steps()).rope_append(q, k, v, positions, inv_freq, slots, k_cache, v_cache, scale, interleaved, inverse,
+                                             offset, q_out)
+    if type(r) is int:
+        _check(r, "moe_rope")
+    return r
 
 
 def moe_linear_int4_workspace_size(M, N, K, group, gated=False) -> int:
     return int(load().moe_linear_int4_workspace_size(M, N, K, group, 1 if gated else 0))
-
-
-@functools.lru_cache(maxsize=256)
-def _linear_workspace(M, N, K, group, gated):
-    return moe_linear_int4_workspace_size(M, N, K, group, gated)
 
 
 def moe_linear_int4(x, w, w_scale, gated=False, out=None, workspace=None):
@@ -627,48 +538,14 @@ def moe_linear_int4(x, w, w_scale, gated=False, out=None, workspace=None):
 
     gated: w holds 2N rows, gate rows first; SiLU(gate) * up of shape [M, N].  See include/gbmoe.h.
     """
-    dtype = x.dtype
-    dt = _float_dtype(x, "x", (0, 1))
-    dev = x.get_device()
-    if x.dim() != 2 or w.dim() != 2 or w_scale.dim() != 2:
-        raise ValueError("x, w and w_scale must have two dimensions")
-    (M, K), (rows, half), (srows, groups) = x.shape, w.shape, w_scale.shape
-    N = rows // 2 if gated else rows
-    if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=x.device)
-    xs, x1 = x.stride()
-    os_, o1 = out.stride()
-    if not (half * 2 == K and srows == rows and groups > 0 and K % groups == 0 and (not gated or rows % 2 == 0)
-            and w.dtype is torch.uint8 and w_scale.dtype is torch.float32 and w.get_device() == dev
-            and w_scale.get_device() == dev and w.is_contiguous() and w_scale.is_contiguous() and out.dtype is dtype
-            and out.get_device() == dev and out.shape == (M, N) and (x1 == 1 or K == 1) and (o1 == 1 or N == 1)):
-        _fail(dev, (x, dtype, (M, K), "x", False), (w, torch.uint8, (None, K // 2), "w", True),
-              (w_scale, torch.float32, (rows, None), "w_scale", True), (out, dtype, (M, N), "out", False))
-    group, ws, ws_bytes = K // groups, 0, 0
-    if workspace is None and (M > 8 or K > 8192):
-        n = _linear_workspace(M, N, K, group, bool(gated))
-        if n:
-            workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
-    if workspace is not None:
-        ws, ws_bytes = workspace.data_ptr(), workspace.numel()
-    st = (_lib or load()).moe_linear_int4(dt, x.data_ptr(), xs if M > 1 else K, w.data_ptr(), w_scale.data_ptr(), M, N,
-                                          K, group, 1 if gated else 0, out.data_ptr(), os_ if M > 1 else N, ws,
-                                          ws_bytes, _raw_stream(dev))
-    if st:
-        _check(st, "moe_linear_int4")
-    return out
+    r = (_steps or _load_steps()).linear_int4(x, w, w_scale, gated, out, workspace)
+    if type(r) is int:
+        _check(r, "moe_linear_int4")
+    return r
 
 
 def moe_tree_attention_workspace_size(nodes, batch, q_heads, k_heads, dim) -> int:
     return int(load().moe_tree_attention_workspace_size(nodes, batch, q_heads, k_heads, dim))
-
-
-@functools.lru_cache(maxsize=256)
-def _tree_workspace(nodes, batch, q_heads, k_heads, dim):
-    n = moe_tree_attention_workspace_size(nodes, batch, q_heads, k_heads, dim)
-    if n == 0:
-        raise MoEError(2, "moe_tree_attention_workspace_size", "unsupported sizes")
-    return n
 
 
 def moe_tree_attention(q, k_cache, v_cache, block_table, context_lens, node_offsets, tree_mask=None, scale=None,
@@ -679,50 +556,11 @@ def moe_tree_attention(q, k_cache, v_cache, block_table, context_lens, node_offs
     context_lens int32 [batch]; node_offsets int32 [batch + 1]; tree_mask int64 / uint64 [nodes] (None: chains);
     scale defaults to dim ** -0.5.
     """
-    dtype = q.dtype
-    dt = _float_dtype(q, "q", (0, 1))
-    dev = q.get_device()
-    if q.dim() != 3 or k_cache.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("q must be [nodes, q_heads, dim], the caches [pages, page_size, k_heads, dim], "
-                         "block_table [batch, pages of a sequence]")
-    N, hq, D = q.shape
-    pages, page, hk, dk = cache = k_cache.shape
-    B, width = block_table.shape
-    if out is None:
-        out = torch.empty((N, hq, D), dtype=dtype, device=q.device)
-    qt, qh, q1 = q.stride()
-    ot, oh, o1 = out.stride()
-    kp, ks, kh, k1 = k_cache.stride()
-    vp, vs, vh, v1 = v_cache.stride()
-    tld, t1 = block_table.stride()
-    i32 = torch.int32
-    if not (dk == D and cache == v_cache.shape and out.shape == q.shape and q1 == o1 == k1 == v1 == 1
-            and (t1 == 1 or width <= 1) and k_cache.dtype is dtype and v_cache.dtype is dtype and out.dtype is dtype
-            and block_table.dtype is i32 and context_lens.dtype is i32 and node_offsets.dtype is i32
-            and context_lens.shape == (B,) and node_offsets.shape == (B + 1,) and context_lens.is_contiguous()
-            and node_offsets.is_contiguous() and k_cache.get_device() == dev and v_cache.get_device() == dev
-            and out.get_device() == dev and block_table.get_device() == dev and context_lens.get_device() == dev
-            and node_offsets.get_device() == dev):
-        _fail(dev, (q, dtype, (N, hq, D), "q", False), (out, dtype, (N, hq, D), "out", False),
-              (k_cache, dtype, (None, None, None, D), "k_cache", False), (v_cache, dtype, tuple(cache), "v_cache", False),
-              (block_table, i32, (B, width), "block_table", False), (context_lens, i32, (B,), "context_lens", True),
-              (node_offsets, i32, (B + 1,), "node_offsets", True))
-    mask = 0
-    if tree_mask is not None:
-        if not ((tree_mask.dtype is torch.int64 or tree_mask.dtype is torch.uint64) and tree_mask.shape == (N,)
-                and tree_mask.is_contiguous() and tree_mask.get_device() == dev):
-            raise ValueError("tree_mask must be a contiguous 64-bit CUDA tensor with one word a node")
-        mask = tree_mask.data_ptr()
-    if workspace is None:
-        workspace = torch.empty(_tree_workspace(N, B, hq, hk, D) if B else 256, dtype=torch.uint8, device=q.device)
-    args = _TREE_ARGS.pack(dt, N, B, hq, hk, D, page, pages, width, D ** -0.5 if scale is None else scale, tld,
-                           q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-                           context_lens.data_ptr(), node_offsets.data_ptr(), mask, out.data_ptr(), qt, qh, ot, oh, kp,
-                           ks, kh, vp, vs, vh)
-    st = (_lib or load()).moe_tree_attention(args, workspace.data_ptr(), workspace.numel(), _raw_stream(dev))
-    if st:
-        _check(st, "moe_tree_attention")
-    return out
+    r = (_steps or _load_steps()).tree_attention(q, k_cache, v_cache, block_table, context_lens, node_offsets, tree_mask,
+                                                scale, out, workspace)
+    if type(r) is int:
+        _check(r, "moe_tree_attention")
+    return r
 
 
 def moe_read_tree_status(workspace: torch.Tensor):
@@ -740,47 +578,8 @@ def moe_verify_draft(target_probs, tokens, node_offsets, coins, last_coins, max_
     coins fp32 [nodes + batch]; last_coins fp32 [batch]; draft_probs fp32 [nodes, vocab] (chains only).
     Returns (out_tokens [batch, max_nodes + 1], path [batch, max_nodes], accepted [batch]), int32.
     """
-    dev = target_probs.get_device()
-    if target_probs.dim() != 2:
-        raise ValueError("target_probs must be [nodes + batch, vocab]")
-    (R, V), N, B = target_probs.shape, tokens.numel(), last_coins.numel()
-    device, i32, f32 = target_probs.device, torch.int32, torch.float32
-    if out_tokens is None:
-        out_tokens = torch.empty((B, max_nodes + 1), dtype=i32, device=device)
-    if path is None:
-        path = torch.empty((B, max_nodes), dtype=i32, device=device)
-    if accepted is None:
-        accepted = torch.empty((B,), dtype=i32, device=device)
-    ts, t1 = target_probs.stride()
-    if not (dev >= 0 and R == N + B and (t1 == 1 or V == 1) and target_probs.dtype is f32 and tokens.dtype is i32
-            and node_offsets.dtype is i32 and coins.dtype is f32 and last_coins.dtype is f32
-            and tokens.shape == (N,) and node_offsets.shape == (B + 1,) and coins.shape == (R,)
-            and last_coins.shape == (B,) and tokens.is_contiguous() and node_offsets.is_contiguous()
-            and coins.is_contiguous() and last_coins.is_contiguous() and tokens.get_device() == dev
-            and node_offsets.get_device() == dev and coins.get_device() == dev and last_coins.get_device() == dev
-            and out_tokens.shape == (B, max_nodes + 1) and path.shape == (B, max_nodes) and accepted.shape == (B,)
-            and out_tokens.dtype is i32 and path.dtype is i32 and accepted.dtype is i32
-            and out_tokens.is_contiguous() and path.is_contiguous() and accepted.is_contiguous()
-            and out_tokens.get_device() == dev and path.get_device() == dev and accepted.get_device() == dev):
-        _fail(dev, (target_probs, f32, (N + B, None), "target_probs", False), (tokens, i32, (N,), "tokens", True),
-              (node_offsets, i32, (B + 1,), "node_offsets", True), (coins, f32, (N + B,), "coins", True),
-              (last_coins, f32, (B,), "last_coins", True), (out_tokens, i32, (B, max_nodes + 1), "out_tokens", True),
-              (path, i32, (B, max_nodes), "path", True), (accepted, i32, (B,), "accepted", True))
-    pp = dp = ds = 0
-    if parents is not None:
-        if not (parents.dtype is i32 and parents.shape == (N,) and parents.is_contiguous()
-                and parents.get_device() == dev):
-            _fail_tensor(parents, dev, i32, (N,), "parents", True)
-        pp = parents.data_ptr()
-    if draft_probs is not None:
-        if not (draft_probs.dtype is f32 and draft_probs.shape == (N, V) and draft_probs.get_device() == dev
-                and (V == 1 or draft_probs.stride(1) == 1)):
-            _fail_tensor(draft_probs, dev, f32, (N, V), "draft_probs", False)
-        dp, ds = draft_probs.data_ptr(), max(draft_probs.stride(0), V)
-    st = (_lib or load()).moe_verify_draft(target_probs.data_ptr(), max(ts, V), dp, ds, tokens.data_ptr(), pp,
-                                           node_offsets.data_ptr(), coins.data_ptr(), last_coins.data_ptr(), B, N, V,
-                                           max_nodes, out_tokens.data_ptr(), path.data_ptr(), accepted.data_ptr(),
-                                           _raw_stream(dev))
-    if st:
-        _check(st, "moe_verify_draft")
-    return out_tokens, path, accepted
+    r = (_steps or _load_steps()).verify_draft(target_probs, tokens, node_offsets, coins, last_coins, max_nodes, parents,
+                                              draft_probs, out_tokens, path, accepted)
+    if type(r) is int:
+        _check(r, "moe_verify_draft")
+    return r

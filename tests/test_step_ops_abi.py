@@ -1,7 +1,7 @@
 """Host-side checks of the decode-step operators: refusals, size queries, frequency tables and the packed argument
 structs.  No call here reaches a launch."""
-import ctypes
 import math
+import struct
 
 import numpy as np
 import pytest
@@ -11,6 +11,9 @@ from _step_ops import fixed60, verify_ref
 from mixture_experts_ffn_moe_gb300 import build, gbmoe
 
 P = 4096  # never dereferenced
+# moe_rope_args_t and moe_tree_attention_args_t, as the C compiler lays them out
+ROPE_ARGS = struct.Struct("@9if2i3P3P3P6q5q3q")
+TREE_ARGS = struct.Struct("@9ifq3P3PPP4q6q")
 
 
 @pytest.fixture(scope="module")
@@ -26,7 +29,7 @@ ROPE = dict(dtype=0, tokens=4, dim=128, rot=128, off=0, inter=0, inv=0, hq=4, hk
 def rope(lib, **kw):
     d = {**ROPE, **kw}
     strides = d.pop("strides", [512, 128, 256, 128, 256, 128, 512, 128, 0, 256, 128, 0, 0, 0])
-    return lib.moe_rope(gbmoe._ROPE_ARGS.pack(*d.values(), *strides), None)
+    return lib.moe_rope(ROPE_ARGS.pack(*d.values(), *strides), None)
 
 
 def test_rope_refusals(lib):
@@ -86,7 +89,7 @@ TREE = dict(dtype=0, nodes=8, batch=2, hq=4, hk=2, dim=128, page=16, pages=10, w
 def tree(lib, ws=P, size=1 << 40, **kw):
     d = {**TREE, **kw}
     strides = d.pop("strides", [512, 128, 512, 128, 4096, 256, 128, 4096, 256, 128])
-    return lib.moe_tree_attention(gbmoe._TREE_ARGS.pack(*d.values(), *strides), ws, size, None)
+    return lib.moe_tree_attention(TREE_ARGS.pack(*d.values(), *strides), ws, size, None)
 
 
 def test_tree_refusals(lib):
@@ -172,7 +175,7 @@ def test_argument_structs_have_the_compilers_size(tmp_path):
                    'sizeof(moe_tree_attention_args_t)); return 0; }\n')
     subprocess.run(["gcc", "-I", build.INCLUDE, str(src), "-o", str(tmp_path / "s")], check=True)
     sizes = subprocess.run([str(tmp_path / "s")], capture_output=True, text=True, check=True).stdout.split()
-    assert [int(v) for v in sizes] == [gbmoe._ROPE_ARGS.size, gbmoe._TREE_ARGS.size]
+    assert [int(v) for v in sizes] == [ROPE_ARGS.size, TREE_ARGS.size]
 
 
 def test_the_reference_sampler_draws_from_the_target():
