@@ -522,7 +522,8 @@ moe_status_t moe_rope(const moe_rope_args_t* args, moe_stream_t stream);
  * block's largest value), sums are fp32, y is rounded once.  Made for the few
  * rows of a decode step (M up to 64 or so); any M is accepted.
  *   workspace    moe_linear_int4_workspace_size(...) bytes, 256-byte aligned; 0
- *                bytes (NULL) for M <= 8 unless K is above 12,000.  Where one is
+ *                bytes (NULL) for M <= 8 with K <= 12,000 and M <= 16 with K <= 5,500
+ *                (M * K that fits into shared memory).  Where one is
  *                used, moe_read_status(workspace) tells whether a device wait gave up.
  */
 size_t moe_linear_int4_workspace_size(int M, int N, int K, int group, int gated);

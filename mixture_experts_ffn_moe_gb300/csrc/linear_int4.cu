@@ -11,7 +11,7 @@
 // each 8 values paired (k0,k4) (k1,k5) (k2,k6) (k3,k7) as the codes come out of their words.  Like the layer's
 // weight-only paths it is kept as fp16 in power-of-two frames, one per token and block: the block's largest |x|
 // lies in [2^14, 2^15), so what fp16 rounds off is below 2^-39 of it, far below the fp32 sums.
-//  * Up to 8 tokens whose x fits: every CTA (persistent, one an SM) does that itself into shared memory, where x
+//  * Up to 16 tokens whose x fits: every CTA (persistent, one an SM) does that itself into shared memory, where x
 //    stays for all of its tiles: one launch.
 //  * Otherwise a first kernel writes them to the workspace for the tcgen05 kernel (linear_int4_wide.cu).
 //
@@ -294,17 +294,18 @@ __device__ __forceinline__ void join_and_write(const LinearArgs& a, const float 
   }
 }
 
-// Up to 8 tokens, x in shared memory.
-template <int G, int RT, int NW>
+// Up to NT * 8 tokens, x in shared memory.
+template <int G, int NT, int RT, int NW>
 __global__ void __launch_bounds__(NW * 32, 1) linear_int4_kernel(LinearArgs a) {
   constexpr int P = Lanes<G>::P, U = kInFlight<RT>;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int odd;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = lane & 3;
   float* red = reinterpret_cast<float*>(smem);
-  uint4* xf = reinterpret_cast<uint4*>(smem + NW * 8 * (RT * 16 + 4) * 4);
+  uint4* xf = reinterpret_cast<uint4*>(smem + NW * NT * 8 * (RT * 16 + 4) * 4);  // [block][token tile][4][32]
   const int nblk = (a.K + kKBlock - 1) / kKBlock;
-  float* sums = reinterpret_cast<float*>(xf + nblk * 128);
+  float* sums = reinterpret_cast<float*>(xf + nblk * NT * 128);                   // [block][P + 1][NT * 8]
+  constexpr int LD = NT * 8;
   pdl_trigger();
   if (tid == 0) odd = 0;
   Stream<G, RT, NW> st(a, warp, lane);
@@ -336,52 +337,55 @@ __global__ void __launch_bounds__(NW * 32, 1) linear_int4_kernel(LinearArgs a) {
       const PieceOfX x = make_piece(v[k], a.bf16);
       if (i < pieces) {
         const int c = i & 15, p = c / (G / 8), cp = c % (G / 8);
-        xf[b * 128 + (p * (4 / P) + cp % (G / 32)) * 32 + m * 4 + cp / (G / 32)] = x.h;
-        if (c == 0) sums[(b * (P + 1) + P) * 8 + m] = x.factor;
+        xf[(b * NT + (m >> 3)) * 128 + (p * (4 / P) + cp % (G / 32)) * 32 + (m & 7) * 4 + cp / (G / 32)] = x.h;
+        if (c == 0) sums[(b * (P + 1) + P) * LD + m] = x.factor;
       }
     }
   }
   __syncthreads();
   // the groups' sums: products with rows of ones (16 where the pieces stand divided by 16)
-  for (int b = warp; b < nblk; b += NW) {
+  for (int bn = warp; bn < nblk * NT; bn += NW) {
+    const int b = bn / NT, m = bn % NT * 8 + 2 * t;
     const uint32_t ones[4] = {0x3c003c00u, 0x3c003c00u, 0x4c004c00u, 0x4c004c00u};
 #pragma unroll
     for (int p = 0; p < P; ++p) {
       float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < 4 / P; ++j) {
-        const uint4 x = xf[b * 128 + (p * (4 / P) + j) * 32 + lane];
+        const uint4 x = xf[bn * 128 + (p * (4 / P) + j) * 32 + lane];
         mma_f16_16816(d, ones, x.x, x.y);
         mma_f16_16816(d, ones, x.z, x.w);
       }
-      if (lane < 4) {  // row 0, tokens 2t and 2t + 1
-        *reinterpret_cast<float2*>(sums + (b * (P + 1) + p) * 8 + 2 * t) = make_float2(d[0] * kMinusBias, d[1] * kMinusBias);
-        if ((2 * t < a.M && !(fabsf(d[0]) < INFINITY)) || (2 * t + 1 < a.M && !(fabsf(d[1]) < INFINITY))) odd = 1;
+      if (lane < 4) {  // row 0, tokens m and m + 1
+        *reinterpret_cast<float2*>(sums + (b * (P + 1) + p) * LD + m) = make_float2(d[0] * kMinusBias, d[1] * kMinusBias);
+        if ((m < a.M && !(fabsf(d[0]) < INFINITY)) || (m + 1 < a.M && !(fabsf(d[1]) < INFINITY))) odd = 1;
       }
     }
   }
   __syncthreads();
   const bool plain = !odd;
   for (int it = 0, tile = blockIdx.x; tile < st.tiles; ++it, tile += gridDim.x) {
-    float acc[RT][1][4];
+    float acc[RT][NT][4];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[r][0][i] = 0.f;
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.f;
     int blk = st.start(it);
     auto run = [&](auto p) {
       for (int rd = 0; rd < st.rounds; rd += U)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           if (blk < nblk)
-            multiply<G, 1, RT, decltype(p)::value>(buf[u], acc, sums + blk * (P + 1) * 8, 8, t,
-                                                   [&](int, int j) { return xf[blk * 128 + j * 32 + lane]; });
+            multiply<G, NT, RT, decltype(p)::value>(buf[u], acc, sums + blk * (P + 1) * LD, LD, t,
+                                                    [&](int n, int j) { return xf[(blk * NT + n) * 128 + j * 32 + lane]; });
           blk += st.wk;
           st.fetch(buf[u], t);
         }
     };
     if (plain) run(std::true_type{}); else run(std::false_type{});
-    join_and_write<1, RT, NW>(a, acc, red, tile, st.wk, st.gated, 0, a.M);
+    join_and_write<NT, RT, NW>(a, acc, red, tile, st.wk, st.gated, 0, a.M);
   }
 }
 
@@ -410,8 +414,10 @@ __global__ void __launch_bounds__(256) linear_pieces_kernel(LinearArgs a) {
   }
 }
 
-// Blocks of K that a CTA of the one-launch kernel can hold.
-template <int G> constexpr int kResidentBlocks = static_cast<int>((kLinearSmem - 16 * 8 * 36 * 4) / (2048 + (Lanes<G>::P + 1) * 32));
+// Blocks of K that a CTA of the one-launch kernel can hold for nt tiles of 8 tokens.
+int resident_blocks(int group, int nt) {
+  return static_cast<int>((kLinearSmem - 16 * nt * 8 * 36 * 4) / (static_cast<size_t>(nt) * (2048 + (128 / group + 1) * 32)));
+}
 
 // Warps that share a tile's blocks: the split of least time, counted in blocks a warp (a tile's join costs one).
 int choose_wr(const LinearArgs& a, int RW, int NW, int sms) {
@@ -426,7 +432,7 @@ int choose_wr(const LinearArgs& a, int RW, int NW, int sms) {
   return wr;
 }
 
-template <int G, int RT>
+template <int G, int NT, int RT>
 cudaError_t launch_resident(LinearArgs a, int sms, cudaStream_t s) {
   constexpr int NW = 16;
   const int RW = a.gated ? 16 : RT * 16, nblk = (a.K + kKBlock - 1) / kKBlock;
@@ -435,10 +441,10 @@ cudaError_t launch_resident(LinearArgs a, int sms, cudaStream_t s) {
   while ((wr << a.wk_log2) < NW) ++a.wk_log2;
   a.tiles = (a.N + RW * wr - 1) / (RW * wr);
   a.tokens_div = fast_div(a.M);
-  auto kern = linear_int4_kernel<G, RT, NW>;
+  auto kern = linear_int4_kernel<G, NT, RT, NW>;
   cudaError_t err = set_smem_limit_once(reinterpret_cast<const void*>(kern), static_cast<int>(kLinearSmem));
   if (err != cudaSuccess) return err;
-  const size_t smem = NW * 8 * (RT * 16 + 4) * 4 + static_cast<size_t>(nblk) * (2048 + (Lanes<G>::P + 1) * 32);
+  const size_t smem = NW * NT * 8 * (RT * 16 + 4) * 4 + static_cast<size_t>(nblk) * NT * (2048 + (Lanes<G>::P + 1) * 32);
   return launch_kernel(kern, dim3(a.tiles < sms ? a.tiles : sms), dim3(NW * 32), smem, s, true, a);
 }
 
@@ -448,15 +454,15 @@ cudaError_t launch_linear(const LinearArgs& a, const WidePlan* wide, int sms, cu
     // 16 or 32 rows a warp: whichever leaves the busiest SM with fewer rows
     const int t1 = (a.N + 15) / 16, t2 = (a.N + 31) / 32;
     const int r1 = (t1 + sms - 1) / sms * 16, r2 = (t2 + sms - 1) / sms * 32;
-    return !a.gated && r1 < r2 ? launch_resident<G, 1>(a, sms, s) : launch_resident<G, 2>(a, sms, s);
+    if (a.M > 8) return launch_resident<G, 2, 2>(a, sms, s);
+    return !a.gated && r1 < r2 ? launch_resident<G, 1, 1>(a, sms, s) : launch_resident<G, 1, 2>(a, sms, s);
   }
   cudaError_t err = launch_kernel(linear_pieces_kernel<G>, dim3((a.K + kKBlock - 1) / kKBlock, a.tokens / 16), dim3(256), 0, s, true, a);
   return err != cudaSuccess ? err : launch_wide_tc(a, G, *wide, s);
 }
 
 bool needs_workspace(int M, int K, int group) {
-  const int fit = group == 128 ? kResidentBlocks<128> : group == 64 ? kResidentBlocks<64> : kResidentBlocks<32>;
-  return M > 8 || (K + kKBlock - 1) / kKBlock > fit;
+  return M > 16 || (K + kKBlock - 1) / kKBlock > resident_blocks(group, M <= 8 ? 1 : 2);
 }
 
 struct LinearLayout { size_t x = 0, sums = 0, part = 0, total = 0; };  // the status words stand first

@@ -237,7 +237,7 @@ PyObject* linear_int4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (given(a[5])) {
       ws = tensor(a[5], "workspace");
       check(ws, &dev, at::kByte, {-1}, "workspace", kContiguous);
-    } else if (M > 0 && (M > 8 || K > 8192)) {
+    } else if (M > 8 || K > 8192) {
       const size_t need = g_linear_workspace(as_int(M, "x"), as_int(N, "w"), as_int(K, "x"), as_int(group, "x"), gated);
       if (need) ws = new_like(x, {static_cast<int64_t>(need)}, at::kByte);
     }

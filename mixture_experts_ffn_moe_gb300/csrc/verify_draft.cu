@@ -114,14 +114,15 @@ __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
   return v;
 }
 
-// A lane's 32 probabilities of the tile at `base` (clamped), all loads in flight: VEC neighbours of every 32 * VEC
-// tokens.
-template <int VEC, bool Q>
+// A lane's 32 probabilities of the tile at `base` (clamped), all loads in flight: 4 neighbours of every 128 tokens, as
+// 16 bytes where rows start on them (VEC).
+constexpr int kGroups = 8;  // of 128 tokens
+template <bool VEC, bool Q>
 __device__ __forceinline__ void load_tile(const float* p, const float* q, int base, int V, int lane, float (&a)[32], float (&b)[32]) {
 #pragma unroll
-  for (int i = 0; i < 32; i += VEC) {
-    const int at = base + (i / VEC * 32 + lane) * VEC;
-    if constexpr (VEC == 4) {
+  for (int i = 0; i < 32; i += 4) {
+    const int at = base + (i / 4 * 32 + lane) * 4;
+    if constexpr (VEC) {
       const bool in = at + 3 < V;  // V is a multiple of 4
       const float4 x = in ? __ldg(reinterpret_cast<const float4*>(p + at)) : make_float4(0.f, 0.f, 0.f, 0.f);
       a[i] = x.x; a[i + 1] = x.y; a[i + 2] = x.z; a[i + 3] = x.w;
@@ -130,8 +131,11 @@ __device__ __forceinline__ void load_tile(const float* p, const float* q, int ba
         b[i] = y.x; b[i + 1] = y.y; b[i + 2] = y.z; b[i + 3] = y.w;
       }
     } else {
-      a[i] = at < V ? __ldg(p + at) : 0.f;
-      if constexpr (Q) b[i] = at < V ? __ldg(q + at) : 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        a[i + j] = at + j < V ? __ldg(p + at + j) : 0.f;
+        if constexpr (Q) b[i + j] = at + j < V ? __ldg(q + at + j) : 0.f;
+      }
     }
   }
 #pragma unroll
@@ -142,7 +146,7 @@ __device__ __forceinline__ void load_tile(const float* p, const float* q, int ba
 }
 
 // The sum of a tile's weights in units of 2^-60 (a lane's share), and the plain sum of its probabilities into fs.
-template <int VEC, bool Q>
+template <bool VEC, bool Q>
 __device__ __forceinline__ uint64_t sum_tile(const float* p, const float* q, int base, int V, int lane, float& fs) {
   float a[32], b[32];
   load_tile<VEC, Q>(p, q, base, V, lane, a, b);
@@ -156,55 +160,51 @@ __device__ __forceinline__ uint64_t sum_tile(const float* p, const float* q, int
 }
 
 // The first token of the tile at `base` with before + (running sum) > level, by a whole warp; -1 if there is none.
-// gone[0..n): tokens of the tile that count nothing.
-template <int VEC, bool Q>
+// Tokens of the n nodes whose parent is `stop` count nothing.
+template <bool VEC, bool Q>
 __device__ __forceinline__ int search_tile(const float* p, const float* q, int base, int V, int lane, uint64_t before, uint64_t level,
                                            const int* tok, const int* par, int n, int stop) {
-  constexpr int NG = 32 / VEC;
   float a[32], b[32];
   load_tile<VEC, Q>(p, q, base, V, lane, a, b);
   for (int j = 0; j < n; ++j)
     if (par[j] == stop && tok[j] >= base && tok[j] < base + kVTile) {
 #pragma unroll
       for (int i = 0; i < 32; ++i)
-        if (base + (i / VEC * 32 + lane) * VEC + i % VEC == tok[j]) a[i] = 0.f;
+        if (base + (i / 4 * 32 + lane) * 4 + i % 4 == tok[j]) a[i] = 0.f;
     }
-  // tokens in order: groups of 32 * VEC, in them VEC a lane.  The groups' sums do not wait for each other.
+  // tokens in order: groups of 128, in them 4 a lane.  The groups' sums do not wait for each other.
+  uint64_t grp[kGroups];
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i) {
+    Levels l;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) add_weight<Q>(l, a[i * 4 + j], b[i * 4 + j]);
+    grp[i] = integer<Q>(l, 4);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) grp[i] += __shfl_xor_sync(0xffffffffu, grp[i], o);
   int at = -1;
-  float ga[VEC], gb[VEC];
+  float ga[4], gb[4];
 #pragma unroll
-  for (int i0 = 0; i0 < NG; i0 += 8) {
-    uint64_t grp[8];
+  for (int i = 0; i < kGroups; ++i) {
+    if (at >= 0) continue;
+    if (before + grp[i] > level) {
+      at = i;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      Levels l;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) add_weight<Q>(l, a[(i0 + i) * VEC + j], b[(i0 + i) * VEC + j]);
-      grp[i] = integer<Q>(l, VEC);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) grp[i] += __shfl_xor_sync(0xffffffffu, grp[i], o);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (at >= 0) continue;
-      if (before + grp[i] > level) {
-        at = i0 + i;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          ga[j] = a[(i0 + i) * VEC + j];
-          if constexpr (Q) gb[j] = b[(i0 + i) * VEC + j];
-        }
-      } else {
-        before += grp[i];
+      for (int j = 0; j < 4; ++j) {
+        ga[j] = a[i * 4 + j];
+        if constexpr (Q) gb[j] = b[i * 4 + j];
       }
+    } else {
+      before += grp[i];
     }
   }
   if (at < 0) return -1;
-  uint64_t w[VEC], run = 0;
+  uint64_t w[4], run = 0;
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) {
+  for (int j = 0; j < 4; ++j) {
     Levels l;
     add_weight<Q>(l, ga[j], gb[j]);
     w[j] = integer<Q>(l, 1);
@@ -219,10 +219,10 @@ __device__ __forceinline__ int search_tile(const float* p, const float* q, int b
   const unsigned hit = __ballot_sync(0xffffffffu, before + run > level);
   const int who = __ffs(hit) - 1;  // the group's last lane at the latest
   uint64_t sum = before + run - own;
-  int x = base + (at * 32 + lane) * VEC;
+  int x = base + (at * 32 + lane) * 4;
   bool here = false;
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) {
+  for (int j = 0; j < 4; ++j) {
     sum += w[j];
     if (!here && sum > level) { here = true; x += j; }
   }
@@ -243,7 +243,7 @@ struct Shared {
   int found;
 };
 
-template <int VEC>
+template <bool VEC>
 __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyArgs a) {
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
@@ -280,7 +280,9 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyArgs a) {
   const bool bad = sh.bad != 0;
   if (!bad && tid < n) {  // a sibling's repeat has no share of its own
     bool again = false;
-    for (int j = 0; j < tid; ++j) again = again || (sh.par[j] == sh.par[tid] && sh.tok[j] == sh.tok[tid]);
+    const int my_par = sh.par[tid], my_tok = sh.tok[tid];
+#pragma unroll 8
+    for (int j = 0; j < tid; ++j) again |= (sh.par[j] == my_par) & (sh.tok[j] == my_tok);
     sh.again[tid] = again;
   }
   __syncthreads();
@@ -290,8 +292,9 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyArgs a) {
       taken = static_cast<double>(coin) * static_cast<double>(q) < static_cast<double>(sh.p[tid]);
     } else {
       uint64_t before = 0;  // the earlier siblings' shares
-      for (int j = 0; j < tid; ++j)
-        if (sh.par[j] == sh.par[tid] && !sh.again[j]) before += sh.share[j];
+      const int my_par = sh.par[tid];
+#pragma unroll 8
+      for (int j = 0; j < tid; ++j) before += sh.par[j] == my_par && !sh.again[j] ? sh.share[j] : 0;
       const uint64_t c = fraction64(coin) >> 4;
       taken = !sh.again[tid] && c >= before && c < before + sh.share[tid];
     }
@@ -447,6 +450,6 @@ extern "C" moe_status_t moe_verify_draft(const float* target_probs, int64_t targ
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return launched("moe_verify_draft", vec ? cudaLaunchKernelEx(&cfg, verify_kernel<4>, a) : cudaLaunchKernelEx(&cfg, verify_kernel<1>, a));
+    return launched("moe_verify_draft", vec ? cudaLaunchKernelEx(&cfg, verify_kernel<true>, a) : cudaLaunchKernelEx(&cfg, verify_kernel<false>, a));
   });
 }
