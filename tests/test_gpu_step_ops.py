@@ -509,3 +509,61 @@ def test_operators_follow_the_current_stream():
         y = gbmoe.moe_linear_int4(xd, wd, sd)
     s.synchronize()
     close(y, *linear_ref(x, w, sc, False))
+
+
+# ------------------------------------------------------------------ the binding's refusals
+def test_bindings_refuse_wrong_tensors():
+    x, w = torch.zeros(2, 256, dtype=BF, device="cuda"), torch.zeros(8, 128, dtype=torch.uint8, device="cuda")
+    s = torch.zeros(8, 2, device="cuda")
+    for bad in (lambda: gbmoe.moe_linear_int4(x.float(), w, s), lambda: gbmoe.moe_linear_int4(x, w[:, :64], s),
+                lambda: gbmoe.moe_linear_int4(x, w, s.cpu()), lambda: gbmoe.moe_linear_int4(x, w, s[:7]),
+                lambda: gbmoe.moe_linear_int4(x.T, w, s), lambda: gbmoe.moe_linear_int4(x, w[:7], s[:7], True),
+                lambda: gbmoe.moe_linear_int4(x, w, s, out=torch.zeros(2, 9, dtype=BF, device="cuda")),
+                lambda: gbmoe.moe_linear_int4(x, w, None)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(gbmoe.MoEError) as e:  # a group size of 8
+        gbmoe.moe_linear_int4(x, w, torch.zeros(8, 32, device="cuda"))
+    assert e.value.status == 2 and "group" in str(e.value)
+    with pytest.raises(gbmoe.MoEError) as e:  # a workspace that is too small
+        gbmoe.moe_linear_int4(torch.zeros(20, 256, dtype=BF, device="cuda"), w, s,
+                              workspace=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 3
+    q, pos = torch.zeros(3, 2, 64, dtype=BF, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    f, _ = gbmoe.rope_frequencies(64)
+    for bad in (lambda: gbmoe.moe_rope(q, None, pos.long(), f), lambda: gbmoe.moe_rope(q, None, pos[:2], f),
+                lambda: gbmoe.moe_rope(q, None, pos, f.float()), lambda: gbmoe.moe_rope(q, q[:, :, :32], pos, f),
+                lambda: gbmoe.moe_rope(q.transpose(1, 2), None, pos, f), lambda: gbmoe.moe_rope(q[0], None, pos, f)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(gbmoe.MoEError):  # a turning part wider than the head
+        gbmoe.moe_rope(q[..., :32], None, pos, f)
+    cache = torch.zeros(4, 16, 1, 64, dtype=BF, device="cuda")
+    table, one = torch.zeros(1, 4, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    offs = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    for bad in (lambda: gbmoe.moe_tree_attention(q, cache.half(), cache, table, one, offs),
+                lambda: gbmoe.moe_tree_attention(q, cache, cache[:3], table, one, offs),
+                lambda: gbmoe.moe_tree_attention(q, cache, cache, table.long(), one, offs),
+                lambda: gbmoe.moe_tree_attention(q, cache, cache, table, one, offs[:1]),
+                lambda: gbmoe.moe_tree_attention(q, cache, cache, table, one, offs, pos)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(gbmoe.MoEError):  # 2 query heads cannot share 3 KV heads
+        gbmoe.moe_tree_attention(q, torch.zeros(4, 16, 3, 64, dtype=BF, device="cuda"),
+                                 torch.zeros(4, 16, 3, 64, dtype=BF, device="cuda"), table, one, offs)
+
+
+def test_empty_calls_return_empty_results():
+    f, _ = gbmoe.rope_frequencies(64)
+    z = torch.zeros(0, dtype=torch.int32, device="cuda")
+    q, k = gbmoe.moe_rope(torch.zeros(0, 2, 64, dtype=BF, device="cuda"), None, z, f)
+    assert q.shape == (0, 2, 64) and k is None
+    w, s = torch.zeros(8, 128, dtype=torch.uint8, device="cuda"), torch.zeros(8, 2, device="cuda")
+    assert gbmoe.moe_linear_int4(torch.zeros(0, 256, dtype=FP, device="cuda"), w, s).shape == (0, 8)
+    cache = torch.zeros(4, 16, 1, 64, dtype=BF, device="cuda")
+    out = gbmoe.moe_tree_attention(torch.zeros(0, 2, 64, dtype=BF, device="cuda"), cache, cache, z.view(0, 4), z,
+                                   torch.zeros(1, dtype=torch.int32, device="cuda"))
+    assert out.shape == (0, 2, 64)
+    out, path, acc = gbmoe.moe_verify_draft(torch.zeros(0, 9, device="cuda"), z, torch.zeros(1, dtype=torch.int32, device="cuda"),
+                                            z.float(), z.float(), 3)
+    assert out.shape == (0, 4) and path.shape == (0, 3) and acc.shape == (0,)
