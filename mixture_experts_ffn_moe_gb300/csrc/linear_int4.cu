@@ -24,6 +24,12 @@
 //
 // Each group's sum is scaled by its row's scale in fp32; the only rounding to 16 bits is the one of y.  The warps
 // that share a tile's rows split K and meet in shared memory in a fixed order: results do not depend on scheduling.
+//
+// Measured: 8 rows, 129,280 x 7168 (495 MB) in 103 us = 4.8 TB/s, with the integer pipe half busy and every lane's rows a line
+// of its own for L1 (16-byte loads of 8 rows a quarter-warp); 4 rows, gated, 2 x 2048 x 7168 in 7.6 us and 1 row, 7168 x 7168
+// (27 MB) in 9.2 us, of which bringing x into order takes 2 to 3 us and the first weights' latency 2 us; 13 rows,
+// 11,003 x 4000 in groups of 32 in 19.5 us (its codes come in loads of 4 bytes).  16 values a thread when x is brought in: a
+// thread with 8 spent 14,000 cycles on 8 rows of 7168, most of them on indices and frames.
 #include <cuda_runtime.h>
 
 #include <type_traits>
@@ -57,34 +63,20 @@ template <int G, int RT> struct Block {
   float s[RT][2];  // of group t of the block (t < P), shared in the quad
 };
 
-// One piece: 8 values of x by one of the 16 neighbouring threads of a block and token (all 16 take part): the values in
-// their frame and order, and the frame's factor.
-struct PieceOfX {
-  uint4 h;
-  float factor;
-};
-__device__ __forceinline__ PieceOfX make_piece(uint4 v, bool bf16) {
-  // magnitudes of either type are ordered like their bit patterns: the largest of the block, two at a time
-  uint32_t top = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-  top = max(top & 0xffffu, top >> 16);
-  const int fe = x_frame_exp(bf16 ? Elem<__nv_bfloat16>::unpack(top).x : Elem<__half>::unpack(top).x);
-  const float mul = exp2i(-fe), low = mul * 0.0625f;
-  const uint32_t e[4] = {v.x, v.y, v.z, v.w};
-  float f[8];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 q = bf16 ? Elem<__nv_bfloat16>::unpack(e[j]) : Elem<__half>::unpack(e[j]);
-    f[2 * j] = q.x;
-    f[2 * j + 1] = q.y;
-  }
-  PieceOfX r;
-  // (k0,k4) (k1,k5)/16 (k2,k6) (k3,k7)/16
-  r.h = make_uint4(pack_half2(f[0] * mul, f[4] * mul), pack_half2(f[1] * low, f[5] * low),
-                   pack_half2(f[2] * mul, f[6] * mul), pack_half2(f[3] * low, f[7] * low));
-  r.factor = exp2i(fe + 12);
-  return r;
+// Magnitudes of 16-bit floats are ordered like their bit patterns: the largest of 8, two at a time.
+__device__ __forceinline__ uint32_t top_of(uint4 v) {
+  return __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+}
+// Exponent of the frame of a block with these largest magnitudes.
+template <typename T> __device__ __forceinline__ int frame_of(uint32_t top) {
+  return x_frame_exp(Elem<T>::unpack(max(top & 0xffffu, top >> 16)).x);
+}
+// 8 neighbouring values in their frame and order: (k0,k4) (k1,k5)/16 (k2,k6) (k3,k7)/16.
+template <typename T> __device__ __forceinline__ uint4 make_piece(uint4 v, float mul) {
+  const float low = mul * 0.0625f;
+  const float2 f01 = Elem<T>::unpack(v.x), f23 = Elem<T>::unpack(v.y), f45 = Elem<T>::unpack(v.z), f67 = Elem<T>::unpack(v.w);
+  return make_uint4(pack_half2(f01.x * mul, f45.x * mul), pack_half2(f01.y * low, f45.y * low),
+                    pack_half2(f23.x * mul, f67.x * mul), pack_half2(f23.y * low, f67.y * low));
 }
 // The sum of a group's values of one token (its G / 8 neighbouring threads' pieces), in the frame.
 template <int G>
@@ -311,51 +303,68 @@ __global__ void __launch_bounds__(NW * 32, 1) linear_int4_kernel(LinearArgs a) {
   Stream<G, RT, NW> st(a, warp, lane);
   pdl_wait();
 
-  // x: 16 neighbouring threads a block and token.  Tokens past the last one are left as they are: columns of a product
-  // do not mix.  The first loads of x and of the weights are under way together.
-  constexpr int B = 4;  // loads in flight a thread
-  const int pieces = nblk * a.M * 16;
-  uint4 v[B];
+  // x: 8 neighbouring threads a block and token, two pieces of it each.  Tokens past the last one are left as they are:
+  // columns of a product do not mix.  The first loads of x and of the weights are under way together.
+  constexpr int B = 2;
+  const int units = nblk * a.M * 8;
+  uint4 v[B][2];
   auto load_x = [&](int w0) {
 #pragma unroll
     for (int k = 0; k < B; ++k) {
-      const int i = w0 + lane + k * NW * 32, b = div_by(i >> 4, a.tokens_div), m = (i >> 4) - b * a.M, col = b * kKBlock + (i & 15) * 8;
-      v[k] = make_uint4(0, 0, 0, 0);
-      if (i < pieces && col < a.K) v[k] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ldx + col);
+      const int i = w0 + lane + k * NW * 32, b = div_by(i >> 3, a.tokens_div), m = (i >> 3) - b * a.M, col = b * kKBlock + (i & 7) * 8;
+      const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ldx + col);
+      v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
+      if (i < units && col < a.K) v[k][0] = at[0];
+      if (i < units && col + 64 < a.K) v[k][1] = at[8];
     }
   };
   load_x(warp * 32);
   Block<G, RT> buf[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) st.fetch(buf[u], t);
-  for (int w0 = warp * 32; w0 < pieces; w0 += B * NW * 32) {  // whole warps: the threads of a piece talk to each other
-    if (w0 != warp * 32) load_x(w0);
+  auto stage = [&](auto type) {
+    using T = decltype(type);
+    for (int w0 = warp * 32; w0 < units; w0 += B * NW * 32) {  // whole warps: the threads of a block talk to each other
+      if (w0 != warp * 32) load_x(w0);
 #pragma unroll
-    for (int k = 0; k < B; ++k) {
-      const int i = w0 + lane + k * NW * 32, b = div_by(i >> 4, a.tokens_div), m = (i >> 4) - b * a.M;
-      if (w0 + k * NW * 32 >= pieces) break;
-      const PieceOfX x = make_piece(v[k], a.bf16);
-      if (i < pieces) {
-        const int c = i & 15, p = c / (G / 8), cp = c % (G / 8);
-        xf[(b * NT + (m >> 3)) * 128 + (p * (4 / P) + cp % (G / 32)) * 32 + (m & 7) * 4 + cp / (G / 32)] = x.h;
-        if (c == 0) sums[(b * (P + 1) + P) * LD + m] = x.factor;
+      for (int k = 0; k < B; ++k) {
+        if (w0 + k * NW * 32 >= units) break;
+        uint32_t top = __vmaxu2(top_of(v[k][0]), top_of(v[k][1]));
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const int i = w0 + lane + k * NW * 32, b = div_by(i >> 3, a.tokens_div), m = (i >> 3) - b * a.M;
+        const int fe = frame_of<T>(top), c = i & 7;
+        const float mul = exp2i(-fe);
+        if (i < units) {
+          uint4* to = xf + (b * NT + (m >> 3)) * 128 + (m & 7) * 4;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int p = (c + 8 * h) / (G / 8), cp = (c + 8 * h) % (G / 8);
+            to[(p * (4 / P) + cp % (G / 32)) * 32 + cp / (G / 32)] = make_piece<T>(v[k][h], mul);
+          }
+          if (c == 0) sums[(b * (P + 1) + P) * LD + m] = exp2i(fe + 12);
+        }
       }
     }
-  }
+  };
+  if (a.bf16) stage(__nv_bfloat16{}); else stage(__half{});
   __syncthreads();
   // the groups' sums: products with rows of ones (16 where the pieces stand divided by 16)
+#pragma unroll 2
   for (int bn = warp; bn < nblk * NT; bn += NW) {
     const int b = bn / NT, m = bn % NT * 8 + 2 * t;
     const uint32_t ones[4] = {0x3c003c00u, 0x3c003c00u, 0x4c004c00u, 0x4c004c00u};
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      float d[4] = {0.f, 0.f, 0.f, 0.f};
+      float d[4] = {0.f, 0.f, 0.f, 0.f}, e[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < 4 / P; ++j) {
         const uint4 x = xf[bn * 128 + (p * (4 / P) + j) * 32 + lane];
         mma_f16_16816(d, ones, x.x, x.y);
-        mma_f16_16816(d, ones, x.z, x.w);
+        mma_f16_16816(e, ones, x.z, x.w);
       }
+      d[0] += e[0];
+      d[1] += e[1];
       if (lane < 4) {  // row 0, tokens m and m + 1
         *reinterpret_cast<float2*>(sums + (b * (P + 1) + p) * LD + m) = make_float2(d[0] * kMinusBias, d[1] * kMinusBias);
         if ((m < a.M && !(fabsf(d[0]) < INFINITY)) || (m + 1 < a.M && !(fabsf(d[1]) < INFINITY))) odd = 1;
@@ -398,14 +407,19 @@ __global__ void __launch_bounds__(256) linear_pieces_kernel(LinearArgs a) {
   const int b = blockIdx.x, c = threadIdx.x & 15, col = b * kKBlock + c * 8, m = blockIdx.y * 16 + (threadIdx.x >> 4);
   uint4 v = make_uint4(0, 0, 0, 0);
   if (m < a.M && col < a.K) v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.x) + m * a.ldx + col);
-  const PieceOfX x = make_piece(v, a.bf16);
-  const float sum = sum_of_group<G>(x.h);
+  uint32_t top = top_of(v);
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int fe = a.bf16 ? frame_of<__nv_bfloat16>(top) : frame_of<__half>(top);
+  const float mul = exp2i(-fe);
+  const uint4 x = a.bf16 ? make_piece<__nv_bfloat16>(v, mul) : make_piece<__half>(v, mul);
+  const float sum = sum_of_group<G>(x);
   const int part = m / a.mt, mp = m - part * a.mt;
   float* sums = a.sums + (static_cast<long long>(b) * (a.tokens / a.mt) + part) * ((P + 1) * a.mt + 4);
   if (m < a.M) {
-    a.xf[static_cast<long long>(m) * gridDim.x * 16 + b * 16 + c] = x.h;
+    a.xf[static_cast<long long>(m) * gridDim.x * 16 + b * 16 + c] = x;
     if (c % (G / 8) == 0) sums[c / (G / 8) * a.mt + mp] = sum * kMinusBias;
-    if (c == 0) sums[P * a.mt + mp] = x.factor;
+    if (c == 0) sums[P * a.mt + mp] = exp2i(fe + 12);
   }
   const bool odd = __syncthreads_or(!(fabsf(sum) < INFINITY) && m < a.M);
   if (threadIdx.x == 0) {
@@ -451,10 +465,12 @@ cudaError_t launch_resident(LinearArgs a, int sms, cudaStream_t s) {
 template <int G>
 cudaError_t launch_linear(const LinearArgs& a, const WidePlan* wide, int sms, cudaStream_t s) {
   if (!wide) {
-    // 16 or 32 rows a warp: whichever leaves the busiest SM with fewer rows
+    // 16 or 32 rows a warp: whichever leaves the busiest SM with fewer rows.  With two token tiles 16 rows take about a
+    // quarter more instructions a row, so they have to save more: 16 tokens, 7168 x 5376: 14.7 us (32 rows: 16.8), 2048 x 4096:
+    // 8.3 us (9.8); 13 tokens, 11003 x 4000 in groups of 32 (80 rows instead of 96): 19.8 us (19.3).
     const int t1 = (a.N + 15) / 16, t2 = (a.N + 31) / 32;
     const int r1 = (t1 + sms - 1) / sms * 16, r2 = (t2 + sms - 1) / sms * 32;
-    if (a.M > 8) return launch_resident<G, 2, 2>(a, sms, s);
+    if (a.M > 8) return !a.gated && 5 * r1 < 4 * r2 ? launch_resident<G, 2, 1>(a, sms, s) : launch_resident<G, 2, 2>(a, sms, s);
     return !a.gated && r1 < r2 ? launch_resident<G, 1, 1>(a, sms, s) : launch_resident<G, 1, 2>(a, sms, s);
   }
   cudaError_t err = launch_kernel(linear_pieces_kernel<G>, dim3((a.K + kKBlock - 1) / kKBlock, a.tokens / 16), dim3(256), 0, s, true, a);
