@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax: one thread a row
     regs_inc<192>();
-    const int i = warp >> 2, r_in = tid & 127;
+    const int i = warp >> 2, r_in = tid & 127, row0 = warp * 32;  // row0: the warp's first row
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // 32 * (warp % 4) in the lane field
     const uint32_t s_tm = tmem + lanes + i * 128, o_tm = tmem + lanes + 256 + i * D;
     int n = 0, piece = 0, done = 0;  // tiles of the CTA, pieces, tiles of this half
@@ -170,18 +170,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u.rows == 0) continue;
       const int row = i * 128 + r_in;
       const bool mine = i == 0 || u.rows > 128;  // has this half any row?
-      // Q_i into shared memory (rows past the last are zeros)
+      // Q_i into shared memory, every warp its own 32 rows (rows past the last one repeat it: nothing
+      // is taken from them), without a branch around the loads, so that all are under way at once
       if (mine) {
-        for (int c = r_in; c < 128 * CH; c += 128) {
-          const int r = c / CH, ch = c % CH;
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (i * 128 + r < u.rows) {
-            const int node = div_by(u.row0 + i * 128 + r, a.group);
-            const int hq = u.head * a.group.d + (u.row0 + i * 128 + r - node * a.group.d);
-            v = ld_v4(static_cast<const T*>(a.q) + (u.node0 + node) * a.q_t + hq * a.q_h + ch * 8);
-            if (negate) { v.x ^= 0x80008000u; v.y ^= 0x80008000u; v.z ^= 0x80008000u; v.w ^= 0x80008000u; }
+        constexpr int B = 8;
+#pragma unroll 1
+        for (int x = 0; x < CH; x += B) {
+          uint4 v[B];
+#pragma unroll
+          for (int k = 0; k < B; ++k) {
+            const int c = (x + k) * 32 + lane, r = u.row0 + min(row0 + c / CH, u.rows - 1), ch = c % CH;
+            const int node = div_by(r, a.group), hq = u.head * a.group.d + (r - node * a.group.d);
+            v[k] = ld_v4(static_cast<const T*>(a.q) + (u.node0 + node) * a.q_t + hq * a.q_h + ch * 8);
           }
-          *reinterpret_cast<uint4*>(qs + i * C::kTileBytes + (ch >> 3) * HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+#pragma unroll
+          for (int k = 0; k < B; ++k) {
+            const int c = (x + k) * 32 + lane, r = (row0 & 127) + c / CH, ch = c % CH;
+            if (negate) { v[k].x ^= 0x80008000u; v[k].y ^= 0x80008000u; v[k].z ^= 0x80008000u; v[k].w ^= 0x80008000u; }
+            *reinterpret_cast<uint4*>(qs + i * C::kTileBytes + (ch >> 3) * HALF + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v[k];
+          }
         }
       }
       if (tid == 0) sm.odd[piece & 1] = 0;
@@ -314,18 +321,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o[e] = __float_as_uint(fmaf(pk, Elem<T>::to_float(vr[c * 32 + e]), __uint_as_float(o[e])));
             }
           }
-          if (live) {
-            if (whole) {
+          if (whole) {
+            if (live) {
               T* dst = static_cast<T*>(a.out) + (u.node0 + node) * a.o_t + hq * a.o_h + c * 32;
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
                 *reinterpret_cast<uint2*>(dst + e) = make_uint2(Elem<T>::pack(__uint_as_float(o[e]) * inv, __uint_as_float(o[e + 1]) * inv),
                                                                 Elem<T>::pack(__uint_as_float(o[e + 2]) * inv, __uint_as_float(o[e + 3]) * inv));
-            } else {
-              float* dst = a.part_o + (slot * a.rows + row) * D + c * 32;
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(dst + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
+          } else {  // parts leave in whole lines, through the 4 KB of the warp's rows of Q_i
+            unsigned char* turn = qs + i * C::kTileBytes + (row0 & 127) * 128;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<uint4*>(turn + lane * 128 + ((e ^ (lane & 7)) << 4)) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int r = k * 4 + (lane >> 3), e = lane & 7;
+              if (row0 + r < u.rows)
+                *reinterpret_cast<uint4*>(a.part_o + (slot * a.rows + row0 + r) * D + c * 32 + e * 4) =
+                    *reinterpret_cast<const uint4*>(turn + r * 128 + ((e ^ (r & 7)) << 4));
+            }
+            __syncwarp();
           }
         }
         if (live && !whole) *reinterpret_cast<float2*>(a.part_ml + (slot * a.rows + row) * 2) = make_float2(m, l);
