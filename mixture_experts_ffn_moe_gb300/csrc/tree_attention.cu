@@ -101,27 +101,27 @@ __global__ void __launch_bounds__(kAThreads, 2)
     const T* vbase = static_cast<const T*>(a.vc) + head * a.v_head;
     const int32_t* table = a.table + b * a.table_ld;
 
-    // The block table entry of this lane's slot of tile `it` (TMA: of its box, lane = box), a tile ahead of its use.
-    int next_page = -1, next_at = 0;
+    // The block table entry of this lane's slot of tile `it` (TMA: of its box, lane = box), before its use.
+    struct Place { int page, at; };
     auto look_up = [&](int it) {
       const int slot = it * kTile + warp * 16 + (TMA ? lane * a.box : lane);
-      next_page = -1;
+      Place p{-1, 0};
       if (it < k1 && lane < (TMA ? (a.box == 16 ? 1 : 2) : 16) && slot < L) {
         const int pi = div_by(slot, a.page);
-        next_at = slot - pi * a.page.d;
-        next_page = __ldg(table + pi);
+        p.at = slot - pi * a.page.d;
+        p.page = __ldg(table + pi);
       }
+      return p;
     };
-    // this warp's 16 slots of tile `it` (looked up before) into stage `st`
-    auto issue = [&](int it, int st) {
-      const int at = next_at;
-      int page = next_page;
+    // this warp's 16 slots of tile `it`, which lie at `place`, into stage `st`
+    auto issue = [&](int it, int st, Place place) {
+      const int at = place.at;
+      int page = place.page;
       if (page < 0 || page >= a.pages) {
         const int slot = it * kTile + warp * 16 + (TMA ? lane * a.box : lane);
         if (lane < (TMA ? (a.box == 16 ? 1 : 2) : 16) && slot < L) bad_pages += TMA ? min(a.box, L - slot) : 1;
         page = -1;
       }
-      look_up(it + 1);
       if constexpr (TMA) {
         const int pg = __shfl_sync(0xffffffffu, page, (lane & 15) >> (a.box == 16 ? 4 : 3)), sl = __shfl_sync(0xffffffffu, at, (lane & 15) >> (a.box == 16 ? 4 : 3));
         const uint32_t ok = __ballot_sync(0xffffffffu, lane < 16 && pg >= 0 && it * kTile + warp * 16 + lane < L);
@@ -155,37 +155,41 @@ __global__ void __launch_bounds__(kAThreads, 2)
         }
       }
     };
+    // A unit starts with all of its loads under way at once: places of the first tiles, queries and masks (rows past
+    // the last one repeat it, without a branch around the loads: nothing is taken from them).
     __syncwarp();
-    look_up(k0);
-    int sent = 0;  // tiles of this unit
+    Place first[C::S - 1];
 #pragma unroll
-    for (int s = 0; s < C::S - 1; ++s) {
-      if (k0 + s < k1) { issue(k0 + s, TMA ? stage_of(s) : s); ++sent; }
-      if constexpr (!TMA) cp_commit();
-    }
-
-    // the unit's rows: row r is node r / group, head r % group of the KV head's queries
-    for (int i = tid; i < R * CH; i += kAThreads) {
-      const int r = i / CH, ch = i % CH;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
-        const int node = div_by(row0 + r, a.group), hq = head * a.group.d + (row0 + r - node * a.group.d);
-        v = ld_v4(static_cast<const T*>(a.q) + (node0 + node) * a.q_t + hq * a.q_h + ch * 8);
-      }
-      *reinterpret_cast<uint4*>(qs + r * C::kRow + ((ch ^ (r & 7)) << 4)) = v;
+    for (int s = 0; s < C::S - 1; ++s) first[s] = look_up(k0 + s);
+    Place next = look_up(k0 + C::S - 1);
+    // row r of the unit is node r / group, head r % group of the KV head's queries
+    uint4 qv[R * CH / kAThreads];
+#pragma unroll
+    for (int k = 0; k < R * CH / kAThreads; ++k) {
+      const int i = tid + k * kAThreads, r = row0 + min(i / CH, rows - 1), node = div_by(r, a.group);
+      const int hq = head * a.group.d + (r - node * a.group.d);
+      qv[k] = ld_v4(static_cast<const T*>(a.q) + (node0 + node) * a.q_t + hq * a.q_h + i % CH * 8);
     }
     unsigned long long bits[RT][2];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int row = r * 16 + h * 8 + g;
-        bits[r][h] = 0;
-        if (row < rows) {
-          const int node = div_by(row0 + row, a.group);
-          bits[r][h] = a.mask ? a.mask[node0 + node] : (2ull << node) - 1;
-        }
+        const int node = div_by(row0 + min(r * 16 + h * 8 + g, rows - 1), a.group);
+        bits[r][h] = (2ull << node) - 1;
+        if (a.mask) bits[r][h] = a.mask[node0 + node];
       }
+    int sent = 0;  // tiles of this unit
+#pragma unroll
+    for (int s = 0; s < C::S - 1; ++s) {
+      if (k0 + s < k1) { issue(k0 + s, TMA ? stage_of(s) : s, first[s]); ++sent; }
+      if constexpr (!TMA) cp_commit();
+    }
+#pragma unroll
+    for (int k = 0; k < R * CH / kAThreads; ++k) {
+      const int i = tid + k * kAThreads, r = i / CH, ch = i % CH;
+      *reinterpret_cast<uint4*>(qs + r * C::kRow + ((ch ^ (r & 7)) << 4)) = qv[k];
+    }
     __syncthreads();
 
     float o[RT][CH][4], m[RT][2], l[RT][2];
@@ -332,7 +336,11 @@ __global__ void __launch_bounds__(kAThreads, 2)
       }
       __syncwarp();
       const int nx = it + C::S - 1;
-      if (nx < k1) { issue(nx, st == 0 ? C::S - 1 : st - 1); ++sent; }
+      if (nx < k1) {
+        issue(nx, st == 0 ? C::S - 1 : st - 1, next);
+        next = look_up(nx + 1);
+        ++sent;
+      }
       if constexpr (!TMA) cp_commit();
       st = st + 1 == C::S ? 0 : st + 1;
       ++used;
@@ -420,12 +428,16 @@ __global__ void __launch_bounds__(128) tree_join_kernel(TreeArgs a) {
   if (row_id >= static_cast<long long>(a.N) * a.Hq) return;
   const int i = static_cast<int>(row_id / a.Hq), hq = static_cast<int>(row_id - static_cast<long long>(i) * a.Hq);
   // the sequence of node i: offsets ascend where they are valid; the checks below leave the rest out
-  int lo = 0, hi = a.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.offs[mid] <= i) lo = mid; else hi = mid;
+  static_assert(kMaxBatch <= 32 * 32, "two steps");
+  const int step = (a.B + 31) / 32;
+  int b = 0;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {  // every step-th sequence, then those in between
+    const int at = b + lane * (s ? 1 : step);
+    const uint32_t before = __ballot_sync(0xffffffffu, (s == 0 || lane < step) && at < a.B && a.offs[min(at, a.B - 1)] <= i);
+    if (before == 0) return;
+    b += (31 - __clz(before)) * (s ? 1 : step);
   }
-  const int b = lo;
   int ctx, n, bd;
   seq_sizes(a, b, ctx, n, bd);
   const int j = i - a.offs[b];
