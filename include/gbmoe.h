@@ -22,7 +22,8 @@
  * Conventions shared by every entry point
  *  - All data pointers are DEVICE pointers owned by the caller.  The library
  *    allocates no memory and never synchronises the stream, except
- *    moe_read_status, which waits for the stream.
+ *    the readers of status words (moe_read_status, moe_read_tree_status,
+ *    moe_read_static_scratch_status), which wait for the stream.
  *  - Every call is enqueued on `stream` (a cudaStream_t; NULL = the legacy
  *    default stream) and is ordered with the caller's other work on it.
  *  - Matrices are row-major and contiguous.
@@ -30,7 +31,7 @@
  *    returned before anything is launched.  A failed launch returns
  *    MOE_ERR_CUDA.  Conditions only the GPU can see (expert ids outside
  *    [0, E)) are counted in a status word inside the workspace; read it with
- *    moe_read_status.
+ *    moe_read_status (tree attention: moe_read_tree_status).
  *  - A flat slot index is i = t * topk + k for token t and top-k column k.
  *  - Calls that share a workspace must not overlap on the GPU.
  */
@@ -53,7 +54,8 @@ typedef enum {
   MOE_ERR_WORKSPACE = 3,   /* workspace NULL, misaligned or smaller than asked */
   MOE_ERR_CUDA = 4,        /* a CUDA runtime call or kernel launch failed      */
   MOE_ERR_TIMEOUT = 5,     /* a bounded device-side wait gave up               */
-  MOE_ERR_BAD_IDS = 6      /* the device saw expert ids outside [0, E)         */
+  MOE_ERR_BAD_IDS = 6      /* the device saw expert ids outside [0, E), or tree attention lengths,
+                              offsets or cache pages out of range              */
 } moe_status_t;
 
 /* flags of fused_moe_fp8 / fused_moe_int8 / fused_moe_int4 / fused_moe_gated */

@@ -25,11 +25,12 @@
 // Each group's sum is scaled by its row's scale in fp32; the only rounding to 16 bits is the one of y.  The warps
 // that share a tile's rows split K and meet in shared memory in a fixed order: results do not depend on scheduling.
 //
-// Measured: 8 rows, 129,280 x 7168 (495 MB) in 103 us = 4.8 TB/s, with the integer pipe half busy and every lane's rows a line
-// of its own for L1 (16-byte loads of 8 rows a quarter-warp); 4 rows, gated, 2 x 2048 x 7168 in 7.6 us and 1 row, 7168 x 7168
-// (27 MB) in 9.2 us, of which bringing x into order takes 2 to 3 us and the first weights' latency 2 us; 13 rows,
-// 11,003 x 4000 in groups of 32 in 19.5 us (its codes come in loads of 4 bytes).  16 values a thread when x is brought in: a
-// thread with 8 spent 14,000 cycles on 8 rows of 7168, most of them on indices and frames.
+// Measured: 8 rows, 129,280 x 7168 (495 MB): 102 us = 4.8 TB/s.  The loads alone take 83 us, bringing x into order 3, and the
+// products' chain (expand, multiply, scale) the rest: four warps a scheduler, which 128 registers a thread allow, do not
+// hide all of it, and the integer pipe is half busy.  More blocks in flight with fewer warps: the same.  4 rows, gated,
+// 2 x 2048 x 7168: 7.6 us; 1 row, 7168 x 7168 (27 MB): 9.2 us, of which launch, x and the first weights' latency are about 5;
+// 13 rows, 11,003 x 4000 in groups of 32 (codes in loads of 4 bytes): 19.5 us.  x is brought in by 16 values a thread: with 8,
+// the indices and frames of 8 rows of 7168 took 14,000 cycles.
 #include <cuda_runtime.h>
 
 #include <type_traits>

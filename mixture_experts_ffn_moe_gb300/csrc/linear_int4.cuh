@@ -13,10 +13,10 @@ struct LinearArgs {
   void* y;             // [M, N], row stride ldy
   long long ldx, ldy;
   int M, N, K, gated, bf16;
-  // up to 8 rows: warps that split the K of a tile (log2; the others take other rows), tiles
+  // one launch: warps that split the K of a tile (log2; the others take other rows), tiles
   int wk_log2, tiles;
   FastDiv tokens_div;
-  // more than 8 rows (workspace): x as the products take it
+  // with a workspace: x as the products take it
   int tokens;          // M rounded up to whole products
   uint4* xf;           // fp16 [tokens][blocks * 128], each 8 columns in the codes' order
   int mt;              // tokens of a product
@@ -41,7 +41,7 @@ __device__ __forceinline__ uint32_t unbias2(uint32_t v, uint32_t bias) {
   return *reinterpret_cast<const uint32_t*>(&q);
 }
 
-// How a call of more than 8 rows is cut (linear_int4_wide.cu).
+// How a call with a workspace is cut (linear_int4_wide.cu).
 struct WidePlan {
   int mt = 0, parts = 0, ctas = 0;  // tokens of a product, parts of the tokens, CTAs a part
   bool cut = false;

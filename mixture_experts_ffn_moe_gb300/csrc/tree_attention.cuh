@@ -134,7 +134,7 @@ __device__ __forceinline__ Piece piece_at(const TreeArgs& a, const long long* pr
   const int span = u.kt + a.setup;
   const int group = a.group.d, per = a.rows * a.ranks, rt_n = (u.n * group + per - 1) / per;
   const long long rel = pos - prefix[u.b];
-  const int unit = static_cast<int>(rel >> 32 ? rel / span : static_cast<uint32_t>(rel) / static_cast<uint32_t>(span)), p0 = static_cast<int>(rel - static_cast<long long>(unit) * span);
+  const int unit = static_cast<int>(rel / span), p0 = static_cast<int>(rel - static_cast<long long>(unit) * span);
   u.places = min(end - pos, static_cast<long long>(span - p0));
   u.k0 = max(0, p0 - a.setup);
   u.k1 = max(0, p0 + static_cast<int>(u.places) - a.setup);

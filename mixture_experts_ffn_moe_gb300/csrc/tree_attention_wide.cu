@@ -16,6 +16,11 @@
 //
 // CTAs whose row tiles belong to the same cache range (up to 4) walk over it side by side, so that HBM delivers it
 // once and L2 the rest.  Every wait is bounded: a role that gives up marks the CTA and all leave.
+//
+// Measured: two documents of 100,003 to 131,072 slots, 64 nodes, 64 / 4 heads of 128: 451 us = 1074 TFLOP/s.  A tile of 128
+// slots takes about 4,300 cycles, of which the thread that issues the products is held back for 3,500: the products of one
+// tile are 2,048 cycles at the full rate, but S reads both of its operands from shared memory at the rate that memory has
+// (8 KB in 64 cycles) while the next tile is written there.  Pairs of SMs that share a tile would halve that traffic.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
