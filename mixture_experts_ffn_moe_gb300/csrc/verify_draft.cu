@@ -267,17 +267,17 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyArgs a) {
   if (!bad_range && tid < n) {
     const int tok = a.tokens[lo + tid], par = a.parents ? a.parents[lo + tid] : tid - 1;
     const bool ok = tok >= 0 && tok < a.V && par >= -1 && par < tid;
+    float p = 0.f;
+    if (ok) {  // (all three loads under way before any is used)
+      p = __ldg(a.target + (row0 + par + 1) * a.ldt + tok);
+      coin = __ldg(a.coins + row0 + par + 1);
+      if (a.draft) q = __ldg(a.draft + (lo + tid) * a.ldd + tok);
+    }
     if (!ok) sh.bad = 1;
     sh.tok[tid] = tok;
     sh.par[tid] = par;
-    sh.p[tid] = 0.f;
-    if (ok) {
-      const float p = a.target[(row0 + par + 1) * a.ldt + tok];
-      sh.p[tid] = p > 0.f ? p : 0.f;
-      sh.share[tid] = integer_of(clamp01(p));
-      coin = a.coins[row0 + par + 1];
-      if (a.draft) q = a.draft[(lo + tid) * a.ldd + tok];
-    }
+    sh.p[tid] = p > 0.f ? p : 0.f;
+    sh.share[tid] = integer_of(clamp01(p));
   }
   __syncthreads();
   const bool bad = sh.bad != 0;
