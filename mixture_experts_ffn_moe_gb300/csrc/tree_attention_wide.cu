@@ -17,10 +17,12 @@
 // CTAs whose row tiles belong to the same cache range (up to 4) walk over it side by side, so that HBM delivers it
 // once and L2 the rest.  Every wait is bounded: a role that gives up marks the CTA and all leave.
 //
-// Measured: two documents of 100,003 to 131,072 slots, 64 nodes, 64 / 4 heads of 128: 451 us = 1074 TFLOP/s.  A tile of 128
-// slots takes about 4,300 cycles, of which the thread that issues the products is held back for 3,500: the products of one
-// tile are 2,048 cycles at the full rate, but S reads both of its operands from shared memory at the rate that memory has
-// (8 KB in 64 cycles) while the next tile is written there.  Pairs of SMs that share a tile would halve that traffic.
+// Measured: two documents of 100,003 to 131,072 slots, 64 nodes, 64 / 4 heads of 128: 451 us = 1074 TFLOP/s; 16 sequences of
+// 2000 slots, 64 nodes, 64 / 8 heads: 127 us.  A tile of 128 slots takes about 4,300 cycles.  The products' pipe is active
+// for 47% of them and a softmax of 128 rows takes 1,400, but the thread that issues the 32 products is held back for 3,450:
+// one of 128 x 128 x 16 takes about 108 cycles instead of 64.  Neither shared memory (34% of its rate) nor the exponentials
+// bound that; it fits a 128-row operand that is fetched before its product instead of under the one before, and only
+// products with more columns, for which tensor memory has no room at D = 128, would hide it.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
