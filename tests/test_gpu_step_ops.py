@@ -150,6 +150,17 @@ def test_linear_int4(M, N, K, group, gated, dt):
     assert torch.equal(y, gbmoe.moe_linear_int4(x.cuda(), w.cuda(), s.cuda(), gated))
 
 
+@pytest.mark.parametrize("M", [1, 8, 9, 16])
+@pytest.mark.parametrize("N,K,group", [(2100, 544, 32), (2431, 192, 64), (4865, 128, 128), (9729, 128, 128), (40, 5504, 64)])
+def test_linear_int4_tiles_of_16_and_32_rows(M, N, K, group):
+    """Widths around the ones where the tile changes, a warp's share of K from a part of a block to many."""
+    g = gen(M + N)
+    x = torch.randn(M, K, generator=g).to(BF)
+    w = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
+    s = (0.5 + torch.rand(N, K // group, generator=g)) * 0.05
+    close(gbmoe.moe_linear_int4(x.cuda(), w.cuda(), s.cuda()), *linear_ref(x, w, s, False))
+
+
 def test_linear_int4_every_code_and_wide_ranges():
     """All 16 codes at every place of a word, scales from 2^-30 to 2^20 and activations from 1e-30 to 1e30."""
     g = gen(2)
@@ -264,6 +275,20 @@ def test_tree_attention(ctx, counts, hq, hk, D, page, dt, masks, hf):
     close(got, *tree_ref(*case, D ** -0.5))
     assert gbmoe.moe_read_tree_status(ws) == (0, 0, 0)
     assert torch.equal(got, run_tree(*case))  # the same bits on another workspace
+
+
+@pytest.mark.parametrize("B,hq,n", [(33, 4, 3), (1024, 2, 2), (65, 64, 9)])
+def test_tree_attention_of_many_sequences_some_of_them_empty(B, hq, n):
+    """Cut units whose sequences stand anywhere among many, between ones without nodes."""
+    r = np.random.default_rng(B)
+    counts = [0 if r.random() < 0.4 else int(r.integers(1, n + 1)) for _ in range(B)]
+    ctx = [int(r.integers(0, 90)) for _ in range(B)]
+    for b in (1, B // 2, B - 1):
+        ctx[b], counts[b] = 3000, n
+    case = make_tree(ctx, counts, hq, 2, 64, 16, BF, B)
+    ws = torch.empty(gbmoe.moe_tree_attention_workspace_size(sum(counts), B, hq, 2, 64), dtype=torch.uint8, device="cuda")
+    close(run_tree(*case, workspace=ws), *tree_ref(*case, 64 ** -0.5))
+    assert gbmoe.moe_read_tree_status(ws) == (0, 0, 0)
 
 
 def test_tree_rows_that_see_nothing_and_empty_sequences():
