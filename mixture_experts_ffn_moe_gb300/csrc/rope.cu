@@ -9,7 +9,7 @@
 // position, and its top 32 bits go to sincospif.  No table of positions is kept.
 //
 // Bound: HBM for prompts (every element is read and written once), launch latency for decode steps.  Measured: 16,384
-// tokens, 64 / 8 heads (302 MB) in 55.8 us = 5.4 TB/s; 32 tokens, 32 / 8 heads with the append in 2.9 us.
+// tokens, 64 / 8 heads (302 MB) in 54.7 us = 5.5 TB/s; 32 tokens, 32 / 8 heads with the append in 2.8 us.
 #include <cuda_runtime.h>
 
 #include "step_ops.cuh"
@@ -39,7 +39,7 @@ struct RopeKernelArgs {
   long long kc_page, kc_slot, kc_head, vc_page, vc_slot, vc_head;
   int tile;              // tokens a CTA turns at once
   int units;             // vectors (or pairs of vectors) of a head that one thread handles in turn
-  FastDiv unit_div;
+  FastDiv unit_div, heads_div;
 };
 
 template <typename T, int V> struct alignas(sizeof(T) * V) Vec { T e[V]; };
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeKernelArgs a) {
     const int work = nt * heads * a.units;
     for (int w = blockIdx.y * kRopeThreads + threadIdx.x; w < work; w += gridDim.y * kRopeThreads) {
       const int hw = div_by(w, a.unit_div), u = w - hw * a.units;
-      const int t = hw / heads, head = hw - t * heads, tok = t0 + t;
+      const int t = div_by(hw, a.heads_div), head = hw - t * heads, tok = t0 + t;
       const T* src;
       T* dst;
       bool turn = u >= unit0 && u < unit0 + turning;
@@ -145,8 +145,9 @@ template <typename T, int V>
 cudaError_t launch_rope(RopeKernelArgs& a, bool inter, int sms, cudaStream_t s) {
   a.units = inter ? a.dim / V : (a.dim - a.rot / 2) / V;
   a.unit_div = fast_div(a.units);
+  a.heads_div = fast_div(a.hq + a.hk + a.hv);
   // up to 4 tokens a CTA: several waves, so that tables are made while other CTAs stream (16384 tokens of 72 x 64
-  // elements, GB300: tiles of 2, 4, 8, 16 59.7, 55.8, 61.7, 61.1 us; 302 MB, 5.4 TB/s)
+  // elements, GB300, one 32-bit division slower than now: tiles of 2, 4, 8, 16 59.7, 55.8, 61.7, 61.1 us)
   int tile = 1;
   while (tile < 4 && static_cast<long long>(a.tokens) > 2LL * sms * tile) tile *= 2;
   while (tile > 1 && (tile + 1) * (a.rot / 2) * 8 > 48 * 1024) tile /= 2;  // the table's shared memory
