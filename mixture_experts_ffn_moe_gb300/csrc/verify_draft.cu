@@ -23,8 +23,8 @@
 // tokens with all of its loads in flight, the CTAs' sums meet through distributed shared memory, and one warp
 // reads the one tile again in which the running sum passes the threshold.
 //
-// Measured: 32 chains of 7 tokens, 129,280 words, with the draft's probabilities: 13.3 us; 2 trees of 24 nodes, 32,003 words:
-// 8.8 us.  The pass over the rows takes about 4 us of the former, the reads that depend on one another the rest.
+// Measured: 32 chains of 7 tokens, 129,280 words, with the draft's probabilities: 13.2 us; 2 trees of 24 nodes, 32,003 words:
+// 8.7 us.  The pass over the rows takes about 4 us of the former, the reads that depend on one another the rest.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
