@@ -111,6 +111,10 @@ __device__ __forceinline__ uint64_t fraction64(float u) {
   return e >= 0 ? m << e : (e < -63 ? 0 : m >> -e);
 }
 
+// The two halves of a cluster barrier: every thread of every CTA arrives, and waits for all of them.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 __device__ __forceinline__ uint64_t warp_sum64(uint64_t v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -254,6 +258,7 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyArgs a) {
   const int b = blockIdx.x / C;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
+  cluster_arrive();  // waited for before the first store to another CTA, on every path
   pdl_wait();
 
   // ---- the nodes: probabilities of every drafted token, gathered at once
@@ -322,6 +327,9 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyArgs a) {
   const int tiles = (a.V + kVTile - 1) / kVTile, per_cta = (tiles + C - 1) / C;
   const int tile0 = min(tiles, rank * per_cta), my_tiles = min(tiles, tile0 + per_cta) - tile0;
   int next = -1;
+  // A CTA's shared memory may be written from outside only once that CTA is known to run: every one has arrived at its
+  // start, so the reads of the nodes hide this wait.
+  cluster_wait();
   // residual: 1 = the draft's share, or the refused children, taken away; 0 = the plain row where nothing is left
   for (int residual = 1; !bad && residual >= 0 && next < 0; --residual) {
     const bool use_q = has_q && residual;

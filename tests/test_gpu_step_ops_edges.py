@@ -1,0 +1,69 @@
+"""GPU tests of the decode-step operators where inputs are unusual but valid, or wrong in a way that a call has to
+notice: broadcast and padded rows, probabilities outside [0, 1], weights far below a row's largest, bad offsets."""
+import numpy as np
+import pytest
+import torch
+
+from _step_ops import verify_ref
+from mixture_experts_ffn_moe_gb300 import build, gbmoe
+
+pytestmark = pytest.mark.gpu
+
+BF, FP, F32, I32 = torch.bfloat16, torch.float16, torch.float32, torch.int32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    build.build()
+    return gbmoe.load()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+# ------------------------------------------------------------------ draft verification
+def probs(rows, V, seed, sharp=3.0):
+    return torch.softmax(torch.randn(rows, V, generator=gen(seed)) * sharp, -1)
+
+
+def verify(target, tokens, offs, coins, last, max_nodes, parents=None, draft=None):
+    return gbmoe.moe_verify_draft(target, torch.tensor(tokens, dtype=I32).cuda(), torch.tensor(offs, dtype=I32).cuda(),
+                                  coins.cuda(), last.cuda(), max_nodes,
+                                  None if parents is None else torch.tensor(parents, dtype=I32).cuda(), draft)
+
+
+def same(got, want):
+    for g, w, name in zip(got, want, ("tokens", "path", "accepted")):
+        assert np.array_equal(g.cpu().numpy(), np.asarray(w)), (name, g.cpu().numpy(), w)
+
+
+@pytest.mark.parametrize("B,n,V", [(12, 5, 40000), (40, 3, 9001), (300, 2, 5000)])
+def test_verify_in_clusters_with_refused_sequences_among_them(B, n, V):
+    """Clusters of 8, 4 and 1 CTAs, replayed from a graph: kept and refused sequences, rows without weight and rows that
+    are no probabilities leave their barriers alike, and every replay gives the same."""
+    g = gen(B)
+    target = probs(B * (n + 1), V, B)
+    target[5 * (n + 1):6 * (n + 1)] = 0.0                 # no weight
+    target[7 * (n + 1):8 * (n + 1)] = 0.5                 # sums far above 1
+    tokens = target.view(B, n + 1, V)[:, :n].argmax(-1)
+    tokens[3, 1] = V                                      # no such token
+    coins, last = torch.rand(B * (n + 1), generator=g), torch.rand(B, generator=g)
+    offs = list(range(0, B * n + 1, n))
+    keep = [b for b in range(B) if b not in (3, 5, 7)]
+    rows = torch.cat([torch.arange(b * (n + 1), (b + 1) * (n + 1)) for b in keep])
+    want = verify_ref(target[rows], tokens[keep].flatten().tolist(), offs[:len(keep) + 1], coins[rows], last[keep], n)
+    args = (target.cuda(), tokens.to(I32).flatten().cuda(), torch.tensor(offs, dtype=I32).cuda(), coins.cuda(), last.cuda(), n)
+    gbmoe.moe_verify_draft(*args)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        results = [gbmoe.moe_verify_draft(*args) for _ in range(4)]
+    for _ in range(20):
+        graph.replay()
+    torch.cuda.synchronize()
+    for got in results:
+        same([t[keep] for t in got], want)
+        assert got[2][[3, 5, 7]].tolist() == [-1, -1, -1] and (got[0][[3, 5, 7]] == -1).all()
