@@ -595,7 +595,8 @@ moe_status_t moe_read_tree_status(const void* workspace, int32_t status_out[2], 
  * After the last kept node the next token is a sample of its row.  A sample of w
  * is the first x with w_0 + .. + w_x > last_coins[b] * sum(w), sums being exact
  * in units of 2^-60 (where a residual has no weight: of the target row).
- *   target_probs fp32 [nodes + batch, vocab], draft_probs fp32 [nodes, vocab]
+ *   target_probs fp32 [nodes + batch, vocab], draft_probs fp32 [nodes, vocab], by
+ *                row strides of at least vocab (no broadcast rows)
  *   tokens, parents int32 [nodes], parents[j] < j counted from the sequence's
  *                first node, -1 for the committed end
  *   coins fp32 [nodes + batch], last_coins fp32 [batch], in [0, 1)

@@ -97,6 +97,9 @@ int as_int(int64_t v, const char* name) {
   if (v > INT_MAX) bad(std::string(name) + " is too large");
   return static_cast<int>(v);
 }
+// The row stride of a matrix: what its tensor says wherever it has rows to step between (the C ABI refuses rows that
+// overlap, such as a broadcast row's stride of 0); of one row or none any stride stands, and its length is given.
+int64_t row_stride(const Tensor& t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
 template <typename T> T* ptr(const Tensor& t) { return static_cast<T*>(t.data_ptr()); }
 moe_stream_t stream_of(const Tensor& t) {
   return reinterpret_cast<moe_stream_t>(c10::cuda::getCurrentCUDAStream(t.device().index()).stream());
@@ -241,8 +244,8 @@ PyObject* linear_int4(PyObject*, PyObject* const* a, Py_ssize_t n) {
       const size_t need = g_linear_workspace(as_int(M, "x"), as_int(N, "w"), as_int(K, "x"), as_int(group, "x"), gated);
       if (need) ws = new_like(x, {static_cast<int64_t>(need)}, at::kByte);
     }
-    if (const moe_status_t st = g_linear(dtype, x.data_ptr(), M > 1 ? x.stride(0) : K, ptr<uint8_t>(w), ptr<float>(s), as_int(M, "x"),
-                                         as_int(N, "w"), as_int(K, "x"), as_int(group, "x"), gated, out.data_ptr(), M > 1 ? out.stride(0) : N,
+    if (const moe_status_t st = g_linear(dtype, x.data_ptr(), row_stride(x), ptr<uint8_t>(w), ptr<float>(s), as_int(M, "x"),
+                                         as_int(N, "w"), as_int(K, "x"), as_int(group, "x"), gated, out.data_ptr(), row_stride(out),
                                          ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.numel() : 0, stream_of(x)))
       return status(st);
     return THPVariable_Wrap(std::move(out));
@@ -336,7 +339,7 @@ PyObject* verify_draft(PyObject*, PyObject* const* a, Py_ssize_t n) {
       const Tensor& d = tensor(a[7], "draft_probs");
       check(d, &dev, at::kFloat, {N, V}, "draft_probs", kRows);
       draft = ptr<float>(d);
-      draft_stride = std::max<int64_t>(d.stride(0), V);
+      draft_stride = row_stride(d);
     }
     if (most < 0) bad("max_nodes must not be negative");
     Tensor out = given(a[8]) ? tensor(a[8], "out_tokens") : new_like(target, {B, most + 1LL}, at::kInt);
@@ -345,7 +348,7 @@ PyObject* verify_draft(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check(out, &dev, at::kInt, {B, most + 1LL}, "out_tokens", kContiguous);
     check(path, &dev, at::kInt, {B, most}, "path", kContiguous);
     check(accepted, &dev, at::kInt, {B}, "accepted", kContiguous);
-    if (const moe_status_t st = g_verify(ptr<float>(target), std::max<int64_t>(target.stride(0), V), draft, draft_stride, ptr<int32_t>(tokens),
+    if (const moe_status_t st = g_verify(ptr<float>(target), row_stride(target), draft, draft_stride, ptr<int32_t>(tokens),
                                          parents, ptr<int32_t>(offs), ptr<float>(coins), ptr<float>(last), as_int(B, "last_coins"),
                                          as_int(N, "tokens"), as_int(V, "target_probs"), most, ptr<int32_t>(out), ptr<int32_t>(path),
                                          ptr<int32_t>(accepted), stream_of(target)))

@@ -67,3 +67,41 @@ def test_verify_in_clusters_with_refused_sequences_among_them(B, n, V):
     for got in results:
         same([t[keep] for t in got], want)
         assert got[2][[3, 5, 7]].tolist() == [-1, -1, -1] and (got[0][[3, 5, 7]] == -1).all()
+
+
+@pytest.mark.parametrize("V,pad", [(64, 4), (64, 3), (33, 7)])
+def test_verify_reads_padded_rows(V, pad):
+    g, offs = gen(V + pad), [0, 3, 5]
+    target, draft = probs(7, V, 1), probs(5, V, 2)
+    tokens = [int(row.argmax()) for row in draft]
+    coins, last = torch.rand(7, generator=g), torch.rand(2, generator=g)
+    wide_t, wide_d = torch.full((7, V + pad), 9.0, device="cuda"), torch.full((5, V + pad), 9.0, device="cuda")
+    wide_t[:, :V], wide_d[:, :V] = target.cuda(), draft.cuda()
+    same(verify(wide_t[:, :V], tokens, offs, coins, last, 3, None, wide_d[:, :V]),
+         verify_ref(target, tokens, offs, coins, last, 3, None, draft))
+
+
+@pytest.mark.parametrize("stride", [0, 1, 32, 63])
+def test_verify_refuses_rows_that_overlap(stride):
+    """A broadcast row (stride 0) or rows less than a vocabulary apart.  (The storage behind each view is as large as
+    rows a vocabulary apart would be, so that no reading of the strides leaves it.)"""
+    V, coins, last = 64, torch.full((4,), 0.5), torch.full((1,), 0.5)
+    rows = probs(4, V, 3).cuda()
+    view = rows.as_strided((4, V), (stride, 1))
+    with pytest.raises(gbmoe.MoEError, match="row stride") as e:
+        verify(view, [1, 2, 3], [0, 3], coins, last, 3)
+    assert e.value.status == 1
+    with pytest.raises(gbmoe.MoEError, match="row stride") as e:
+        verify(rows, [1, 2, 3], [0, 3], coins, last, 3, None, view[:3])
+    assert e.value.status == 1
+
+
+def test_verify_takes_a_single_row_of_any_stride():
+    V = 64
+    target, draft = probs(2, V, 4), probs(1, V, 5)
+    coins, last = torch.tensor([0.9, 0.3]), torch.tensor([0.4])
+    one = draft.cuda().as_strided((1, V), (0, 1))
+    same(verify(target.cuda(), [7], [0, 1], coins, last, 1, None, one),
+         verify_ref(target, [7], [0, 1], coins, last, 1, None, draft))
+    row = target[:1].cuda().as_strided((1, V), (1, 1))
+    same(verify(row, [], [0, 0], coins[:1], last, 0), verify_ref(target[:1], [], [0, 0], coins[:1], last, 0))
