@@ -541,7 +541,10 @@ moe_status_t moe_linear_int4(int dtype, const void* x, int64_t x_stride, const u
  * sequence's first) sees every committed slot and slot context + i for each set
  * bit i of its tree_mask word:
  *   out[j, h] = sum_s softmax_s(scale * q[j, h] . K[s, h / g]) V[s, h / g],
- * g = q_heads / k_heads.  Zeros where it sees nothing.
+ * g = q_heads / k_heads.  Zeros where it sees nothing.  Scores, the softmax's
+ * sums and the output's are fp32; a weight is rounded to the caches' type before
+ * it meets V (fp16: in full for weights down to about 2^-21 of the row's largest,
+ * in steps of 2^-31 of it below).
  *   q, out       [nodes, q_heads, dim] by stride_t and stride_h, bf16 or fp16
  *   k_cache, v_cache  [num_pages, page_size, k_heads, dim] by their strides
  *                (any order of the dimensions), the type of q

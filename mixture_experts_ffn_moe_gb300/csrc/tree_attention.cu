@@ -6,8 +6,9 @@
 // reference m, the sum l of 2^(s - m) and the unnormalised output are kept in fp32, and partial results over
 // different slots are joined as (m, l, O).  The reference is moved (and O rescaled) only when a row's maximum has
 // grown by more than 2^8; that leaves the result the same and keeps 2^(s - m) at most 2^8.  A row that sees
-// nothing gives zeros.  P is rounded to the cache's type for the product with V (half a step of that type per
-// term, averaging out over the sum, as the output is itself rounded to it).
+// nothing gives zeros.  P is rounded to the cache's type for the product with V, l is the sum of the unrounded weights: half a
+// step of that type a term, as the output is itself rounded to it.  In fp16 the weights stand 2^7 higher (kHeadroom), since
+// fp16 has few bits for small ones: a slot 2^25 below a row's largest still counts.
 //
 // Bound: K and V are read once: 4 * L * Hkv * D bytes.  The nodes of a tree and the query heads of a KV head
 // are rows of one matrix product, so a cache line serves all of them.
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kAThreads, 2)
 #pragma unroll
             for (int d = 0; d < CH; ++d) { o[r][d][2 * h] *= f; o[r][d][2 * h + 1] *= f; }
           }
-          const float ref = m[r][h] == -INFINITY ? 0.f : m[r][h];
+          const float ref = (m[r][h] == -INFINITY ? 0.f : m[r][h]) - kHeadroom<T>;
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = ex2(v[i] - ref);
           l[r][h] += (v[0] + v[1]) + (v[2] + v[3]);

@@ -12,6 +12,11 @@ constexpr int kMaxTreeCtas = 320;    // CTAs that the workspace has room for
 constexpr int kWideTile = 128;       // slots of a tile and rows of a product of the tcgen05 kernel
 constexpr int kWideRows = 256;       // rows of its row tile
 constexpr float kLazy = 8.f;         // growth of a row's maximum (in powers of two) that moves its reference
+// Powers of two by which all of a row's weights (those of P, of its sum l and of O alike) stand above 2^(s - m).  fp16 holds
+// 2^15, and a weight of at most 2^kLazy leaves 7 of them: so weights down to 2^-21 of the reference keep fp16's full precision
+// in the product with V and those down to 2^-32 do not vanish, instead of 2^-14 and 2^-25.  bf16 has fp32's range.
+template <typename T> constexpr float kHeadroom = 0.f;
+template <> constexpr float kHeadroom<__half> = 15.f - kLazy;
 
 struct TreeArgs {
   const void* q;

@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float ref = m == -INFINITY ? 0.f : m;
+        const float ref = (m == -INFINITY ? 0.f : m) - kHeadroom<T>;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const T* vr = static_cast<const T*>(a.vc) + page * a.v_page + at * a.v_slot + u.head * a.v_head;
               float dot = 0.f;
               for (int d = 0; d < D; ++d) dot = fmaf(Elem<T>::to_float(qr[d]), Elem<T>::to_float(kr[d]), dot);
-              const float pk = ex2(fmaf(negate ? -dot : dot, scale, -(m == -INFINITY ? 0.f : m)));
+              const float pk = ex2(fmaf(negate ? -dot : dot, scale, kHeadroom<T> - (m == -INFINITY ? 0.f : m)));
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 o[e] = __float_as_uint(fmaf(pk, Elem<T>::to_float(vr[c * 32 + e]), __uint_as_float(o[e])));

@@ -4,8 +4,9 @@ import numpy as np
 import pytest
 import torch
 
-from _step_ops import verify_ref
+from _step_ops import tree_ref, verify_ref
 from mixture_experts_ffn_moe_gb300 import build, gbmoe
+from test_gpu_step_ops import _dev, close, make_tree
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +106,30 @@ def test_verify_takes_a_single_row_of_any_stride():
          verify_ref(target, [7], [0, 1], coins, last, 1, None, draft))
     row = target[:1].cuda().as_strided((1, V), (1, 1))
     same(verify(row, [], [0, 0], coins[:1], last, 0), verify_ref(target[:1], [], [0, 0], coins[:1], last, 0))
+
+
+# ------------------------------------------------------------------ tree attention
+@pytest.mark.parametrize("hq,nodes,page", [(2, 3, 16), (2, 3, 5), (8, 6, 16), (8, 6, 5), (32, 8, 16), (32, 8, 5)])
+@pytest.mark.parametrize("dt,D", [(FP, 128), (FP, 64), (BF, 128)])
+def test_tree_attention_weights_far_below_a_rows_largest(hq, nodes, page, dt, D):
+    """Every 16th slot outweighs the others by about 2^25 and has a value of zero: what the result is made of are the small
+    weights, which have to reach the product with V with their bits."""
+    (q, kc, vc, table, ctx, offs, masks), r = make_tree([300], [nodes], hq, 1, D, page, dt, 41, None), gen(42)
+    L = 300 + nodes
+    base = torch.randn(D, generator=r)
+    q = (base + 0.05 * torch.randn(nodes, hq, D, generator=r)).to(dt)
+    top = base / (base @ base) * (25.0 * np.log(2.0) * D ** 0.5)
+    for s in range(L):
+        at = (table[0, s // page], s % page)
+        kc[at] = (top if s % 16 == 5 else 0.02 * torch.randn(D, generator=r)).to(dt)
+        vc[at] = (torch.zeros(D) if s % 16 == 5 else 4000.0 * (0.5 + torch.rand(D, generator=r))).to(dt)
+    ref, bound = tree_ref(q, kc, vc, table, ctx, offs, masks, D ** -0.5)
+    if dt == FP:
+        # P stands with 2^7 on top of a row's reference, which is at most its largest score: half a subnormal step of
+        # 2^-25 is 2^-32 of the largest weight, a slot; the sinks (one in 16 slots) carry the sum
+        sinks = sum(s % 16 == 5 for s in range(300))
+        bound = bound + L * 6000.0 * 2.0 ** -32 * 4 / sinks  # (their scores differ by less than 2 powers of two)
+    got = gbmoe.moe_tree_attention(q.cuda(), _dev(kc), _dev(vc), torch.from_numpy(table).cuda(), torch.tensor(ctx, dtype=I32).cuda(),
+                                   torch.tensor(offs, dtype=I32).cuda())
+    assert (ref > 8 * bound).all()
+    close(got, ref, bound)
