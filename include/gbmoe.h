@@ -608,7 +608,8 @@ moe_status_t moe_read_tree_status(const void* workspace, int32_t status_out[2], 
  *   accepted     int32 [batch] out: number of kept nodes; -1 (and no tokens) for
  *                a sequence with bad offsets, tokens or parents, or whose row has
  *                no weight or a sum above 8
- * Probabilities above 1 count as 1, negative ones and NaN as 0.
+ * Probabilities above 1 count as 1, negative ones and NaN as 0, in the test of a
+ * drafted token as in a sample.
  */
 moe_status_t moe_verify_draft(const float* target_probs, int64_t target_stride, const float* draft_probs,
                               int64_t draft_stride, const int32_t* tokens, const int32_t* parents,

@@ -279,10 +279,12 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyArgs a) {
       if (a.draft) q = __ldg(a.draft + (lo + tid) * a.ldd + tok);
     }
     if (!ok) sh.bad = 1;
+    p = clamp01(p);
+    q = clamp01(q);
     sh.tok[tid] = tok;
     sh.par[tid] = par;
-    sh.p[tid] = p > 0.f ? p : 0.f;
-    sh.share[tid] = integer_of(clamp01(p));
+    sh.p[tid] = p;
+    sh.share[tid] = integer_of(p);
   }
   __syncthreads();
   const bool bad = sh.bad != 0;

@@ -133,3 +133,23 @@ def test_tree_attention_weights_far_below_a_rows_largest(hq, nodes, page, dt, D)
                                    torch.tensor(offs, dtype=I32).cuda())
     assert (ref > 8 * bound).all()
     close(got, ref, bound)
+
+
+def test_verify_counts_probabilities_outside_0_and_1_alike_everywhere():
+    """At the drafted token: NaN and negative values count as 0 and values above 1 as 1, in the test of acceptance as
+    in the sample."""
+    V, odd = 40, [float("nan"), -0.5, 0.0, 0.3, 2.0, 3.0]
+    pairs = [(p, q) for p in odd for q in odd]
+    B = len(pairs)
+    target, draft = probs(2 * B, V, 11), probs(B, V, 12)
+    tokens = [(7 * b) % V for b in range(B)]
+    for b, (p, q) in enumerate(pairs):
+        target[2 * b, tokens[b]] = p
+        draft[b, tokens[b]] = q
+    last = torch.rand(B, generator=gen(13))
+    for coin in (0.0, 0.7):
+        coins = torch.full((2 * B,), coin)
+        plain = [x.nan_to_num(nan=0.0).clamp(0.0, 1.0) for x in (target, draft)]
+        want = verify_ref(plain[0], tokens, list(range(B + 1)), coins, last, 1, None, plain[1])
+        assert 0 < want[2].sum() < B
+        same(verify(target.cuda(), tokens, list(range(B + 1)), coins, last, 1, None, draft.cuda()), want)
