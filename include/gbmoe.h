@@ -606,8 +606,8 @@ moe_status_t moe_read_tree_status(const void* workspace, int32_t status_out[2], 
  *   out_tokens   int32 [batch, max_nodes + 1] out: kept tokens, the next, then -1
  *   path         int32 [batch, max_nodes] out: kept nodes in order, then -1
  *   accepted     int32 [batch] out: number of kept nodes; -1 (and no tokens) for
- *                a sequence with bad offsets, tokens or parents, or whose row has
- *                no weight or a sum above 8
+ *                a sequence with bad offsets, tokens or parents, or where the row
+ *                of the next token has no weight or a sum above 8
  * Probabilities above 1 count as 1, negative ones and NaN as 0, in the test of a
  * drafted token as in a sample.
  */

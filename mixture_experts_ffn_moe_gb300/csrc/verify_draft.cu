@@ -302,11 +302,16 @@ __global__ void __launch_bounds__(kVThreads, 2) verify_kernel(VerifyArgs a) {
       taken = static_cast<double>(coin) * static_cast<double>(q) < static_cast<double>(sh.p[tid]);
     } else {
       uint64_t before = 0;  // the earlier siblings' shares
+      float about = 0.f;    // the same in fp32: 64 bits hold sums below 16
       const int my_par = sh.par[tid];
 #pragma unroll 8
-      for (int j = 0; j < tid; ++j) before += sh.par[j] == my_par && !sh.again[j] ? sh.share[j] : 0;
+      for (int j = 0; j < tid; ++j) {
+        const bool counts = sh.par[j] == my_par && !sh.again[j];
+        before += counts ? sh.share[j] : 0;
+        about += counts ? sh.p[j] : 0.f;
+      }
       const uint64_t c = fraction64(coin) >> 4;
-      taken = !sh.again[tid] && c >= before && c < before + sh.share[tid];
+      taken = !sh.again[tid] && about < 8.f && c >= before && c < before + sh.share[tid];
     }
     if (taken) atomicOr(&sh.taken, 1ull << tid);
   }

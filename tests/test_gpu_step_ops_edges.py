@@ -153,3 +153,16 @@ def test_verify_counts_probabilities_outside_0_and_1_alike_everywhere():
         want = verify_ref(plain[0], tokens, list(range(B + 1)), coins, last, 1, None, plain[1])
         assert 0 < want[2].sum() < B
         same(verify(target.cuda(), tokens, list(range(B + 1)), coins, last, 1, None, draft.cuda()), want)
+
+
+def test_verify_children_past_the_end_of_the_shares_are_never_kept():
+    """Shares that add up to 16 and more (a root row that is no distribution): only what lies in [0, 1) can hold a coin."""
+    V, n = 100, 40
+    target = probs(n + 1, V, 14)
+    for value, coin, kept in ((1.0, 0.25, 0), (0.9, 0.95, 1), (0.4, 0.9, 2)):
+        target[0] = 0.0
+        target[0, :n] = value
+        coins, last = torch.full((n + 1,), coin), torch.tensor([0.6])
+        want = verify_ref(target, list(range(n)), [0, n], coins, last, n, [-1] * n)
+        assert want[2][0] == 1 and want[1][0, 0] == kept
+        same(verify(target.cuda(), list(range(n)), [0, n], coins, last, n, [-1] * n), want)
