@@ -432,21 +432,35 @@ __global__ void __launch_bounds__(128) tree_join_kernel(TreeArgs a) {
   const int lane = threadIdx.x & 31;
   if (row_id >= static_cast<long long>(a.N) * a.Hq) return;
   const int i = static_cast<int>(row_id / a.Hq), hq = static_cast<int>(row_id - static_cast<long long>(i) * a.Hq);
-  // the sequence of node i: offsets ascend where they are valid; the checks below leave the rest out
+  // The sequence of node i: the last one that starts at or before it where all offsets ascend.  Beside offsets that do not,
+  // that can be a sequence without the node (or none); then all of them are asked.
   static_assert(kMaxBatch <= 32 * 32, "two steps");
+  int ctx, n, bd, j;
+  auto owner = [&](int s) {
+    seq_sizes(a, s, ctx, n, bd);
+    j = i - a.offs[s];
+    return j >= 0 && j < n;
+  };
   const int step = (a.B + 31) / 32;
   int b = 0;
 #pragma unroll
   for (int s = 0; s < 2; ++s) {  // every step-th sequence, then those in between
     const int at = b + lane * (s ? 1 : step);
     const uint32_t before = __ballot_sync(0xffffffffu, (s == 0 || lane < step) && at < a.B && a.offs[min(at, a.B - 1)] <= i);
-    if (before == 0) return;
-    b += (31 - __clz(before)) * (s ? 1 : step);
+    b += before ? (31 - __clz(before)) * (s ? 1 : step) : 0;
   }
-  int ctx, n, bd;
-  seq_sizes(a, b, ctx, n, bd);
-  const int j = i - a.offs[b];
-  if (j < 0 || j >= n) return;
+  if (!owner(b)) {
+    uint32_t who = 0;
+    int first = 0;
+    for (; first < a.B; first += 32) {
+      const int s = first + lane;
+      who = __ballot_sync(0xffffffffu, s < a.B && owner(min(s, a.B - 1)));
+      if (who) break;
+    }
+    if (!who) return;
+    b = first + __ffs(who) - 1;
+    owner(b);
+  }
   const int group = a.group.d, head = hq / group, r = j * group + (hq - head * group);
   const int kt = (ctx + n + a.tile - 1) / a.tile, per = a.rows * a.ranks, rt_n = (n * group + per - 1) / per;
   const long long chunk = a.prefix[a.B + 1];

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from _step_ops import tree_ref, verify_ref
+from _step_ops import mask_tensor, tree_ref, verify_ref
 from mixture_experts_ffn_moe_gb300 import build, gbmoe
 from test_gpu_step_ops import _dev, close, make_tree
 
@@ -166,3 +166,24 @@ def test_verify_children_past_the_end_of_the_shares_are_never_kept():
         want = verify_ref(target, list(range(n)), [0, n], coins, last, n, [-1] * n)
         assert want[2][0] == 1 and want[1][0, 0] == kept
         same(verify(target.cuda(), list(range(n)), [0, n], coins, last, n, [-1] * n), want)
+
+
+@pytest.mark.parametrize("hq", [4, 64])
+@pytest.mark.parametrize("before", [0, 40])
+def test_tree_attention_joins_sequences_beside_bad_offsets(hq, before):
+    """Cut units of good sequences are joined whatever the offsets of the others are; rows of bad ones stay as they are."""
+    ctx, counts = [10] * before + [4000, 20, 4000], [1] * before + [4, 4, 4]
+    q, kc, vc, table, ctx, offs, masks = make_tree(ctx, counts, hq, 2, 64, 16, BF, 31)
+    ref, bound = tree_ref(q, kc, vc, table, ctx, offs, masks, 64 ** -0.5)
+    b = before + 2                                       # a sequence more, between the last two: [.., o + 4, -5, o + 8, ..]
+    table = np.insert(table, b, table[before], 0)
+    ctx, offs = ctx[:b] + [50] + ctx[b:], offs[:b] + [-5] + offs[b:]
+    N = q.shape[0]
+    out = torch.full(q.shape, 7.0, dtype=BF, device="cuda")
+    ws = torch.empty(gbmoe.moe_tree_attention_workspace_size(N, len(ctx), hq, 2, 64), dtype=torch.uint8, device="cuda")
+    gbmoe.moe_tree_attention(q.cuda(), _dev(kc), _dev(vc), torch.from_numpy(table).cuda(), torch.tensor(ctx, dtype=I32).cuda(),
+                             torch.tensor(offs, dtype=I32).cuda(), mask_tensor(masks).cuda(), out=out, workspace=ws)
+    good = [i for i in range(N) if not before + 4 <= i < before + 8]
+    close(out[good], ref[good], bound[good])
+    assert (out[before + 4:before + 8] == 7.0).all()
+    assert gbmoe.moe_read_tree_status(ws)[0] == 2
