@@ -476,9 +476,10 @@ moe_status_t moe_profile_read(float* stage_ms, const char** stage_names, int max
  *   y0 = x0 c - x1 s,  y1 = x1 c + x0 s        (inverse != 0: -s for s)
  * interleaved == 0: pair i is (rot_offset + i, rot_offset + rot_dim / 2 + i);
  * interleaved != 0: (rot_offset + 2i, rot_offset + 2i + 1).  Elements outside
- * [rot_offset, rot_offset + rot_dim) are copied.  Angles are exact to
- * |p * inv_freq| * 2^-53 radians at any position (64-bit fractions of a turn);
- * products are fp32, rounded once to the tensors' type.
+ * [rot_offset, rot_offset + rot_dim) are copied.  Angles are 64-bit fractions of
+ * a turn, off by at most |p * inv_freq| * 2^-52 + |p| * 2^-62 radians at any
+ * position; their sines and cosines are right to a few units of the last place of
+ * fp32, products are fp32, rounded once to the tensors' type.
  *
  *   q, k         [tokens, heads, dim] by stride_t and stride_h
  *   q_out, k_out outputs; either may be its input (in place)

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from _step_ops import mask_tensor, tree_ref, verify_ref
+from _step_ops import mask_tensor, rope_ref, tree_ref, verify_ref
 from mixture_experts_ffn_moe_gb300 import build, gbmoe
 from test_gpu_step_ops import _dev, close, make_tree
 
@@ -187,3 +187,25 @@ def test_tree_attention_joins_sequences_beside_bad_offsets(hq, before):
     close(out[good], ref[good], bound[good])
     assert (out[before + 4:before + 8] == 7.0).all()
     assert gbmoe.moe_read_tree_status(ws)[0] == 2
+
+
+# ------------------------------------------------------------------ rotary positions
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_of_unit_vectors_is_right_to_the_last_bits(inter):
+    """Sines and cosines themselves, of any size: an angle keeps its bits near every quarter of a turn and near zero."""
+    f = torch.tensor([2.0 ** -40, 1e-9, 3e-7, 1e-4, 0.37, 1.0, np.pi / 2, np.pi / 2 + 1e-6, 1.5, 100.25, np.pi, 2 * np.pi,
+                      np.pi / 4, np.nextafter(np.pi / 4, 0.0), np.nextafter(np.pi / 4, 1.0)], dtype=torch.float64)
+    half, pos = len(f), torch.tensor([0, 1, 2, 3, 7, -1, -1000, 4096, 99991, 1 << 20, 2 ** 31 - 1], dtype=I32)
+    x = torch.zeros(len(pos), 2, 2 * half)
+    first = slice(0, 2 * half, 2) if inter else slice(0, half)
+    second = slice(1, 2 * half, 2) if inter else slice(half, 2 * half)
+    x[:, 0, first] = 1.0                                  # (cos, sin)
+    x[:, 1, second] = 1.0                                 # (-sin, cos)
+    got = gbmoe.moe_rope(x.cuda(), None, pos.cuda(), f.cuda(), interleaved=inter)[0].double().cpu()
+    ref, _ = rope_ref(x, pos, f, 1.0, inter, False, 0)
+    # the angle as a 64-bit fraction of a turn: 2^-52 of it (the frequency's conversion) and 2^-62 a position; then the
+    # rest to a quarter turn as fp32 (two roundings of 2^-24 of it), sine and cosine (a unit of the last place, 2^-23);
+    # the scale, the product with 1 and the sum with 0 are exact
+    phase = (pos.double().abs()[:, None] * (f * 2.0 ** -52 + 2.0 ** -62)).repeat(1, 2) if not inter else \
+        (pos.double().abs()[:, None] * (f * 2.0 ** -52 + 2.0 ** -62)).repeat_interleave(2, 1)
+    close(got, ref, ref.abs() * 4 * 2.0 ** -24 + phase[:, None])
