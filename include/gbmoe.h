@@ -521,9 +521,12 @@ moe_status_t moe_rope(const moe_rope_args_t* args, moe_stream_t stream);
  * gated != 0: w and w_scale hold 2N rows, gate rows first, and
  *   y = SiLU(gate) * up.
  * K is a multiple of group; x rows and w start on 16 bytes.  x enters the products
- * as fp16 in a power-of-two frame per row and 128 columns (exact to 2^-39 of the
- * block's largest value), sums are fp32, y is rounded once.  Made for the few
- * rows of a decode step (M up to 64 or so); any M is accepted.
+ * as fp16 in a power-of-two frame per row and 128 columns (exact to 2^-35 of the
+ * block's largest value), codes as q + 8, whose share of 8 sum x is taken off
+ * again: a sum is off by a few units of 2^-24 of sum |x| (q + 16) w_scale, so
+ * a code of 0 under a value that dwarfs its row is not free.  Sums are fp32, y is
+ * rounded once.  Made for the few rows of a decode step (M up to 64 or so); any M
+ * is accepted.
  *   workspace    moe_linear_int4_workspace_size(...) bytes, 256-byte aligned; 0
  *                bytes (NULL) for M <= 8 with K <= 12,000 and M <= 16 with K <= 5,500
  *                (M * K that fits into shared memory).  Where one is

@@ -10,7 +10,8 @@
 // x is brought into the order in which the products take it: per block and 8 tokens four 16-byte pieces a lane,
 // each 8 values paired (k0,k4) (k1,k5) (k2,k6) (k3,k7) as the codes come out of their words.  Like the layer's
 // weight-only paths it is kept as fp16 in power-of-two frames, one per token and block: the block's largest |x|
-// lies in [2^14, 2^15), so what fp16 rounds off is below 2^-39 of it, far below the fp32 sums.
+// lies in [2^14, 2^15), so what fp16 rounds off (half a subnormal step of 2^-25, in the pieces that are stored divided by 16
+// below) is at most 2^-35 of it, far below the fp32 sums.
 //  * Up to 16 tokens whose x fits: every CTA (persistent, one an SM) does that itself into shared memory, where x
 //    stays for all of its tiles: one launch.
 //  * Otherwise a first kernel writes them to the workspace for the tcgen05 kernel (linear_int4_wide.cu).
@@ -19,7 +20,8 @@
 // word one shift): the biased code u = q + 8 stands alone in an fp16 as a subnormal, u * 2^-24, or 16 u * 2^-24
 // where its nibble is the higher one; the tensor cores take subnormals exactly, and the pieces (k1,k5), (k3,k7)
 // of x are stored divided by 16.  sum x u = sum x q + 8 sum x, so the accumulators of a group start at -8 times
-// the group's sum of x (kept beside x).  All of that is exact but for the fp32 sums.  Where x holds an infinity
+// the group's sum of x (kept beside x).  All of that is exact but for the fp32 sums, which thus carry x (q + 8) and 8 x: a few
+// units of 2^-24 of sum |x| (q + 16), where codes without a bias would have them of sum |x q|.  Where x holds an infinity
 // or NaN the bias is subtracted from every code instead, so that they come out as they would.
 //
 // Each group's sum is scaled by its row's scale in fp32; the only rounding to 16 bits is the one of y.  The warps

@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from _step_ops import mask_tensor, rope_ref, tree_ref, verify_ref
+from _step_ops import HALF, TINY, int4_values, mask_tensor, rope_ref, tree_ref, verify_ref
 from mixture_experts_ffn_moe_gb300 import build, gbmoe
 from test_gpu_step_ops import _dev, close, make_tree
 
@@ -209,3 +209,25 @@ def test_rope_of_unit_vectors_is_right_to_the_last_bits(inter):
     phase = (pos.double().abs()[:, None] * (f * 2.0 ** -52 + 2.0 ** -62)).repeat(1, 2) if not inter else \
         (pos.double().abs()[:, None] * (f * 2.0 ** -52 + 2.0 ** -62)).repeat_interleave(2, 1)
     close(got, ref, ref.abs() * 4 * 2.0 ** -24 + phase[:, None])
+
+
+# ------------------------------------------------------------------ 4-bit linear
+@pytest.mark.parametrize("M,N,K,group", [(1, 40, 512, 128), (8, 33, 256, 32), (16, 64, 1024, 64), (40, 70, 640, 128), (33, 40, 320, 64), (64, 40, 96, 32)])
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_linear_int4_with_activations_that_stand_out(M, N, K, group, dt):
+    """A column of every block is 2^12 times the others and meets codes of zero and others: the bound follows what the kernels
+    compute, sums of x (q + 8) less 8 sums of x, both in fp32."""
+    g = gen(M + K)
+    x = torch.randn(M, K, generator=g).to(dt)
+    x[:, 5::128] = (4096.0 * (1.0 + torch.rand(M, (K + 122) // 128, generator=g))).to(dt)
+    w = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
+    w[: N // 2, 2::64] &= 15                              # column 5 is a high nibble: zero for the first rows
+    s = (0.5 + torch.rand(N, K // group, generator=g)) * 0.05
+    q, sc = int4_values(w), s.double().repeat_interleave(group, 1)
+    xd = x.double()
+    ref = xd @ (q * sc).T
+    # products are exact; x (q + 8) and 8 x in at most K / 16 steps each, off by 2^-22 (the steps may truncate) of the
+    # absolute sums; x itself by 2^-35 of its block's largest
+    err = (xd.abs() @ ((q + 8 + 8) * sc).T) * (16 + K / 128) * 2.0 ** -22
+    top = xd.abs().amax(1, keepdim=True) @ (q.abs() * sc).sum(1)[None] * 2.0 ** -35
+    close(gbmoe.moe_linear_int4(x.cuda(), w.cuda(), s.cuda()), ref, err + top + ref.abs() * HALF[dt] + TINY[dt])
