@@ -1,10 +1,11 @@
 """Builds libgbmoe.so (the C-ABI CUDA library) in-tree for sm_103a.
 
 Each .cu file is compiled by its own nvcc process (in parallel), then the
-objects are linked into a shared library next to this file.  The C++ binding of
-the decode-step operators (csrc/step_bindings.cpp, against the installed torch's
-headers) is compiled beside them into _step_bindings.so.  Nothing is installed
-anywhere else.
+objects are linked into a shared library next to this file.  That takes nvcc
+alone.  The C++ binding of the decode-step operators (csrc/step_bindings.cpp,
+against the installed torch's headers) is compiled beside them into
+_step_bindings.so, and again for another torch; without torch, which it serves,
+it is left out.  Nothing is installed anywhere else.
 
     python -m mixture_experts_ffn_moe_gb300.build [--verbose]
 """
@@ -24,6 +25,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgbmoe.so")
 STEPS = os.path.join(PKG, "_step_bindings.so")
+STEPS_TORCH = os.path.join(BUILD, "step_bindings.torch")  # the torch that it was compiled against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -50,7 +52,25 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def _compile_steps() -> None:
+def _torch_version():
+    """Of the installed torch; None where there is none."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return str(torch.__version__)
+
+
+def steps_built_against():
+    """The torch version that _step_bindings.so was compiled against; None where that is not known."""
+    try:
+        with open(STEPS_TORCH) as f:
+            return f.read()
+    except OSError:
+        return None
+
+
+def _compile_steps(version: str) -> None:
     """The Python binding of the decode-step operators, with the host compiler."""
     import sysconfig
 
@@ -70,32 +90,49 @@ def _compile_steps() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"the host compiler failed on step_bindings.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(STEPS + ".tmp", STEPS)
+    with open(STEPS_TORCH, "w") as f:
+        f.write(version)
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(STEPS):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(STEPS))
-    deps = glob.glob(os.path.join(CSRC, "*")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
-    return any(os.path.getmtime(p) > t for p in deps)
+def _older(out: str, sources) -> bool:
+    return not os.path.exists(out) or any(os.path.getmtime(p) > os.path.getmtime(out) for p in sources)
+
+
+def _lib_stale() -> bool:
+    own = [p for p in glob.glob(os.path.join(CSRC, "*")) if not p.endswith(".cpp")]
+    return _older(LIB, own + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__])
+
+
+def _steps_stale(version: str) -> bool:
+    own = glob.glob(os.path.join(CSRC, "*.cpp")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
+    return _older(STEPS, own) or steps_built_against() != version
+
+
+def _link(objs) -> None:
+    tmp = LIB + ".tmp"
+    r = subprocess.run([nvcc(), "-shared", "-o", tmp] + objs + ARCH, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, LIB)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libgbmoe.so and _step_bindings.so if a source is newer; returns the library's path."""
-    if not force and not _stale():
+    """Compile and link libgbmoe.so and _step_bindings.so if a source of theirs is newer; returns the library's path.
+
+    The library is linked whatever becomes of the binding, whose failure is raised afterwards.
+    """
+    version = _torch_version()
+    lib, steps = force or _lib_stale(), version is not None and (force or _steps_stale(version))
+    if not lib and not steps:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        steps = ex.submit(_compile_steps)
-        objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        steps.result()
-    tmp = LIB + ".tmp"
-    cmd = [nvcc(), "-shared", "-o", tmp] + objs + ARCH
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB)
+        binding = ex.submit(_compile_steps, version) if steps else None
+        if lib:
+            _link(list(ex.map(lambda s: _compile(s, verbose), srcs)))
+        if binding:
+            binding.result()
     return LIB
 
 

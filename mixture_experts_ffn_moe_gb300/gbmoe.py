@@ -14,6 +14,8 @@ import os
 
 import torch
 
+from . import build
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgbmoe.so")
 
@@ -455,6 +457,9 @@ def _load_steps():
         lib = load()
         if not os.path.exists(STEPS_PATH):
             raise RuntimeError(f"{STEPS_PATH} is missing: build it with `python -m mixture_experts_ffn_moe_gb300.build`")
+        if build.steps_built_against() != str(torch.__version__):  # its tensors are laid out as that torch's
+            raise RuntimeError(f"{STEPS_PATH} was built against torch {build.steps_built_against()}, this is "
+                               f"{torch.__version__}: build it again with `python -m mixture_experts_ffn_moe_gb300.build`")
         spec = importlib.util.spec_from_file_location("_step_bindings", STEPS_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
