@@ -9,11 +9,19 @@
 // of a block, expands them (5 integer instructions for 8 codes) into tensor memory, and takes the block's sums back
 // into fp32 registers.  Three warpgroups take blocks in turn, so that one expands while another's product runs.
 //
-// The products bound it: with A from tensor memory one of 16 columns takes about 80 cycles whatever the tokens (up to
-// 128), 640 a block, where HBM would deliver a block's 8 KB of codes in 340.  Around it stand the launches: the first
-// kernel takes about 3 us, the join of cut tiles 4.
+// What bounds it is a block's way through the roles.  A warpgroup takes about 3,200 cycles for one: 870 until its codes are
+// there, 590 to expand them, 1,500 for its product in a queue of three, 225 to take the sums; so with three of them one leaves
+// every 1,060.  The products alone take 48 cycles each back to back whatever the tokens up to 64 (64 at 128), 57 to 64 with a
+// commit a block and the warpgroups' traffic to tensor memory beside them: about 500 a block, where HBM would deliver its 8 KB
+// of codes in 340.  Around it stand the launches: the first kernel takes about 3 us, the join of cut tiles 4.
 //
-// Measured, 7168 x 7168 in groups of 128: 16, 32, 64 rows 20.4, 22.9, 28.2 us; 64 rows, 32,768 x 2048: 33 us.
+// More tokens than a product has are further parts, on CTAs of their own, that expand and multiply all of the weights
+// again: 64 tokens a part in groups of 128, 32 in groups of 64, 16 in groups of 32, where every group of a block has sums of
+// its own in tensor memory, for three warpgroups.
+//
+// Measured, 7168 x 7168: groups of 128, 16, 32, 64, 65, 128, 256 rows: 20.4, 22.9, 28.2, 41, 42, 73 us; groups of 64, 16, 32,
+// 33, 64, 128, 256 rows: 21.4, 24.6, 39, 39, 68, 120; groups of 32, 16, 17, 32, 64, 128, 256 rows: 26.4, 42, 43, 76, 139, 286.
+// 64 rows, 32,768 x 2048 in groups of 128: 33 us.
 //
 // The blocks of all tiles form one line, divided evenly over the CTAs where that is faster than whole tiles; a tile
 // that is cut leaves fp32 parts in the workspace that a last kernel adds up in order.  Every wait is bounded.

@@ -18,11 +18,12 @@
 // once and L2 the rest.  Every wait is bounded: a role that gives up marks the CTA and all leave.
 //
 // Measured: two documents of 100,003 to 131,072 slots, 64 nodes, 64 / 4 heads of 128: 451 us = 1074 TFLOP/s; 16 sequences of
-// 2000 slots, 64 nodes, 64 / 8 heads: 127 us.  A tile of 128 slots takes about 4,300 cycles.  The products' pipe is active
-// for 47% of them and a softmax of 128 rows takes 1,400, but the thread that issues the 32 products is held back for 3,450:
-// one of 128 x 128 x 16 takes about 108 cycles instead of 64.  Neither shared memory (34% of its rate) nor the exponentials
-// bound that; it fits a 128-row operand that is fetched before its product instead of under the one before, and only
-// products with more columns, for which tensor memory has no room at D = 128, would hide it.
+// 2000 slots, 64 nodes, 64 / 8 heads: 126 us (pages of 12 slots, by cp.async: 159).  A tile of 128 slots takes about 4,300
+// cycles.  Its 32 products take 2,048 of them (the products' pipe is active for 47%) and a softmax of 128 rows 1,400, but the
+// thread that issues the products is inside their instructions for 3,450.  The products' form is not why: by themselves, back
+// to back, those of 128 x 128 x 16 take 64 cycles each, with the first operand in shared memory or in tensor memory, into one
+// accumulator or two, in this kernel's order or in turn, and with the softmax warps' traffic to tensor memory beside them.
+// Shared memory is at 34% of its rate.  What keeps them apart in here has not been found.
 #include <cuda.h>
 #include <cuda_runtime.h>
 

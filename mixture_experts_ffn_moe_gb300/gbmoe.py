@@ -541,7 +541,8 @@ def moe_linear_int4_workspace_size(M, N, K, group, gated=False) -> int:
 def moe_linear_int4(x, w, w_scale, gated=False, out=None, workspace=None):
     """x [M, K] (bf16 / fp16) times 4-bit weights w uint8 [N, K/2] with w_scale fp32 [N, K/group]: [M, N].
 
-    gated: w holds 2N rows, gate rows first; SiLU(gate) * up of shape [M, N].  See include/gbmoe.h.
+    gated: w holds 2N rows, gate rows first; SiLU(gate) * up of shape [M, N].  workspace: uint8, for callers that keep
+    one (and read its status); without it one is allocated for the call where it takes one.  See include/gbmoe.h.
     """
     r = (_steps or _load_steps()).linear_int4(x, w, w_scale, gated, out, workspace)
     if type(r) is int:
@@ -559,7 +560,8 @@ def moe_tree_attention(q, k_cache, v_cache, block_table, context_lens, node_offs
 
     k_cache, v_cache [pages, page_size, k_heads, dim]; block_table int32 [batch, pages of a sequence];
     context_lens int32 [batch]; node_offsets int32 [batch + 1]; tree_mask int64 / uint64 [nodes] (None: chains);
-    scale defaults to dim ** -0.5.
+    scale defaults to dim ** -0.5.  workspace: uint8, for callers that keep one; only then can moe_read_tree_status tell
+    of bad lengths, offsets or pages afterwards (a workspace allocated for the call is gone with it).
     """
     r = (_steps or _load_steps()).tree_attention(q, k_cache, v_cache, block_table, context_lens, node_offsets, tree_mask,
                                                 scale, out, workspace)
@@ -580,7 +582,8 @@ def moe_verify_draft(target_probs, tokens, node_offsets, coins, last_coins, max_
     """Keeps or refuses drafted tokens and draws the next one (see include/gbmoe.h).
 
     target_probs fp32 [nodes + batch, vocab]; tokens, parents int32 [nodes]; node_offsets int32 [batch + 1];
-    coins fp32 [nodes + batch]; last_coins fp32 [batch]; draft_probs fp32 [nodes, vocab] (chains only).
+    coins fp32 [nodes + batch]; last_coins fp32 [batch]; draft_probs fp32 [nodes, vocab] (chains only).  Rows may be
+    padded but not overlap: expand()ed rows are refused.
     Returns (out_tokens [batch, max_nodes + 1], path [batch, max_nodes], accepted [batch]), int32.
     """
     r = (_steps or _load_steps()).verify_draft(target_probs, tokens, node_offsets, coins, last_coins, max_nodes, parents,
