@@ -175,16 +175,26 @@ __global__ void __launch_bounds__(kNWarps * 32) norm_rope_kernel(const __grid_co
           for (int i = 0; i < V; ++i) sum = fmaf(y[n][p][i], y[n][p][i], sum);
       for (int o = G >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
       float r = rsqrtf(__fdividef(sum, static_cast<float>(a.dim)) + a.eps);
-      if (__any_sync(0xffffffffu, sum == INFINITY)) {  // squares past fp32's range: the sum of (x / 2^64)^2
+      if (__any_sync(0xffffffffu, sum == INFINITY)) {
+        // squares past fp32's range: the sum of (x / 2^80)^2, in range for 1024 of the largest numbers; x / 2^40 and 2^40 / root
+        // then are normal numbers wherever their product counts
         float small = 0.f;
 #pragma unroll
         for (int n = 0; n < NU; ++n)
 #pragma unroll
           for (int p = 0; p < P; ++p)
 #pragma unroll
-            for (int i = 0; i < V; ++i) small = fmaf(y[n][p][i] * 0x1p-64f, y[n][p][i] * 0x1p-64f, small);
+            for (int i = 0; i < V; ++i) small = fmaf(y[n][p][i] * 0x1p-80f, y[n][p][i] * 0x1p-80f, small);
         for (int o = G >> 1; o > 0; o >>= 1) small += __shfl_xor_sync(0xffffffffu, small, o);
-        if (sum == INFINITY) r = rsqrtf(__fdividef(small, static_cast<float>(a.dim))) * 0x1p-64f;
+        if (sum == INFINITY) {
+          r = rsqrtf(__fdividef(small, static_cast<float>(a.dim))) * 0x1p-40f;
+#pragma unroll
+          for (int n = 0; n < NU; ++n)
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+              for (int i = 0; i < V; ++i) y[n][p][i] *= 0x1p-40f;
+        }
       }
       if (active && wt) {
 #pragma unroll
@@ -487,17 +497,24 @@ __global__ void __launch_bounds__(kNWarps * 32, 5) norm_rope_vec_kernel(const __
         float sum = P == 2 ? (s0.x + s0.y) + (s1.x + s1.y) : s0.x + s0.y;
         for (int o = G >> 1; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         float r = rsqrtf(fmaf(sum, inv_dim, a.eps));
-        if (__any_sync(0xffffffffu, sum == INFINITY)) {  // squares past fp32's range: the sum of (x / 2^64)^2
+        if (__any_sync(0xffffffffu, sum == INFINITY)) {  // squares past fp32's range: as in the kernel above
           float small = 0.f;
 #pragma unroll
           for (int p = 0; p < P; ++p)
 #pragma unroll
             for (int i = 0; i < H; ++i) {
               const float2 f = unpair(y[p][i]);
-              small = fmaf(f.x * 0x1p-64f, f.x * 0x1p-64f, fmaf(f.y * 0x1p-64f, f.y * 0x1p-64f, small));
+              small = fmaf(f.x * 0x1p-80f, f.x * 0x1p-80f, fmaf(f.y * 0x1p-80f, f.y * 0x1p-80f, small));
             }
           for (int o = G >> 1; o > 0; o >>= 1) small += __shfl_xor_sync(0xffffffffu, small, o);
-          if (sum == INFINITY) r = rsqrtf(small * inv_dim) * 0x1p-64f;
+          if (sum == INFINITY) {
+            r = rsqrtf(small * inv_dim) * 0x1p-40f;
+            const uint64_t f = pair(0x1p-40f, 0x1p-40f);
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+              for (int i = 0; i < H; ++i) y[p][i] = mul2(y[p][i], f);
+          }
         }
         const uint64_t rr = pair(r, r);
 #pragma unroll
