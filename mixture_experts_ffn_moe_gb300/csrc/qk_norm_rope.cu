@@ -577,6 +577,9 @@ __global__ void __launch_bounds__(kNWarps * 32, 5) norm_rope_vec_kernel(const __
   section(std::integral_constant<int, 2>(), v0, v1);
 }
 
+// (up to 2^31 - 1 items: their number with what fills the last CTA up is no int)
+unsigned norm_ctas(const NormArgs& a) { return (static_cast<unsigned>(a.items) + kNWarps - 1) / kNWarps; }
+
 template <typename T, bool INTER>
 cudaError_t launch_norm_vec(NormArgs& a, int sms, cudaStream_t s) {
   const int step = 32 / a.lanes, rounds = (a.hq + step - 1) / step + (a.hk + step - 1) / step + (a.hv + step - 1) / step;
@@ -590,7 +593,7 @@ cudaError_t launch_norm_vec(NormArgs& a, int sms, cudaStream_t s) {
   a.pieces = fast_div(real);
   a.items = a.tokens * real;
   const size_t smem = static_cast<size_t>(a.rot / 2) * 8 * (1 + kNWarps);
-  return launch_kernel(norm_rope_vec_kernel<T, INTER>, dim3((a.items + kNWarps - 1) / kNWarps), dim3(kNWarps * 32), smem, s, true, a);
+  return launch_kernel(norm_rope_vec_kernel<T, INTER>, dim3(norm_ctas(a)), dim3(kNWarps * 32), smem, s, true, a);
 }
 
 template <typename T, int V, bool INTER, int NU>
@@ -606,7 +609,7 @@ cudaError_t launch_norm_nu(NormArgs& a, int sms, cudaStream_t s) {
   a.pieces = fast_div(real);
   a.items = a.tokens * real;
   const size_t smem = static_cast<size_t>(a.rot / 2) * 8 * (1 + kNWarps);
-  return launch_kernel(norm_rope_kernel<T, V, INTER, NU>, dim3((a.items + kNWarps - 1) / kNWarps), dim3(kNWarps * 32), smem, s,
+  return launch_kernel(norm_rope_kernel<T, V, INTER, NU>, dim3(norm_ctas(a)), dim3(kNWarps * 32), smem, s,
                        true, a);
 }
 

@@ -38,3 +38,16 @@ def test_norm_rope_of_heads_near_the_largest_numbers(dt, D, inter):
     got, _ = gbmoe.moe_qk_norm_rope(x.cuda(), None, pos.cuda(), f, w.cuda(), None, 1e-6, interleaved=inter)
     y, err = norm_ref(x, w, 1e-6, pos, f.cpu(), 1.0, inter, 0)
     close(got, y, rounded(y, err, dt))
+
+
+def test_norm_rope_of_as_many_heads_as_it_takes():
+    """2^31 - 1 heads of one element: as many pieces of work as an int counts, the last CTA not full."""
+    T, many = 2 ** 31 - 1, 2053
+    f = torch.empty(0, dtype=torch.float64).cuda()
+    w = torch.tensor([1.5], dtype=BF).cuda()
+    x = (torch.randn(many, 1, 1, generator=gen(4)) * 1e-3).to(BF).cuda()
+    want, _ = gbmoe.moe_qk_norm_rope(x, None, torch.zeros(many, dtype=I32).cuda(), f, w, None, 1e-6)
+    q = x.repeat(T // many + 1, 1, 1)[:T]
+    gbmoe.moe_qk_norm_rope(q, None, torch.zeros(T, dtype=I32, device="cuda"), f, w, None, 1e-6, q_out=q)
+    whole = T // many * many
+    assert (q[:whole].view(-1, many) == want.view(1, many)).all() and torch.equal(q[whole:], want[:T - whole])
