@@ -705,7 +705,9 @@ moe_status_t moe_cache_read(const moe_cache_read_args_t* args, moe_stream_t stre
  * such product, in steps of 2^-31 of it below).  Value scales count as brought into
  * [2^-64, 2^64], and those of a sequence's slots and head are taken to lie within a factor
  * of 2^100 of each other (slots far below that lose their share of the softmax's sum);
- * NaN stays NaN.  Infinities and NaN in slots that a node does not see do
+ * NaN stays NaN.  Slots of zero value codes with a scale of 1, as moe_qk_norm_rope writes
+ * them, count with a scale of 2^-40 there and among the products that weights are rounded
+ * by: they add nothing, and values far below 1 keep their bits beside them.  Infinities and NaN in slots that a node does not see do
  * not reach it; a drafted slot whose value codes hold a NaN (0x7f, 0xff) gives NaN in the
  * whole head to the nodes that see it.
  * Code rows start on 16 bytes and their strides are multiples of 16 elements; scales by

@@ -12,6 +12,8 @@ constexpr int kMaxTreeCtas = 320;    // CTAs that the workspace has room for
 constexpr int kHeaderCtas = 480;     // CTAs that its header counts bad pages for
 constexpr int kWideTile = 128;       // slots of a tile and rows of a product of the tcgen05 kernel
 constexpr int kWideRows = 256;       // rows of its row tile
+constexpr float kZeroScale = 1.f;    // value scale of a slot of zero values, and log2 of the one that it counts with
+constexpr float kZeroCounts = -40.f;
 constexpr float kLazy = 8.f;         // growth of a row's maximum (in powers of two) that moves its reference
 // Powers of two by which all of a row's weights (those of P, of its sum l and of O alike) stand above 2^(s - m).  fp16 holds
 // 2^15, and a weight of at most 2^kLazy leaves 7 of them: so weights down to 2^-21 of the reference keep fp16's full precision
@@ -70,6 +72,8 @@ __device__ __forceinline__ float lg2(float x) {
 // Is any of four E4M3 codes NaN (0x7f, 0xff)?
 __device__ __forceinline__ bool has_nan(uint32_t w) { return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0; }
 __device__ __forceinline__ bool has_nan(const uint4& v) { return has_nan(v.x) || has_nan(v.y) || has_nan(v.z) || has_nan(v.w); }
+// Is any of 16 E4M3 codes another than 0 (of either sign)?
+__device__ __forceinline__ bool not_zero(const uint4& v) { return ((v.x | v.y | v.z | v.w) & 0x7f7f7f7fu) != 0; }
 // Words of two 16-bit elements: does either hold an infinity or NaN?
 __device__ __forceinline__ bool nonfinite2(__nv_bfloat16, uint32_t w) {
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;

@@ -17,7 +17,7 @@
 // Over a cache of 8-bit codes (tree_attention_fp8.cu has the mathematics) the loaders' warps bring codes by cp.async to the
 // rows of a tile where they are needed, a tile ahead, and turn them into fp16 in place, which is exact; the products are those
 // of fp16.  The softmax takes three numbers a slot from shared memory: the key's scale, log2 of the value's, and the power of
-// two that takes that off again.  Two documents of 50,003 to 65,536 slots, 64 nodes, 64 / 4 heads of 128: 387 us = 626 TFLOP/s.
+// two that takes that off again.  Two documents of 50,003 to 65,536 slots, 64 nodes, 64 / 4 heads of 128: 390 us = 622 TFLOP/s.
 // There the softmax bounds it: with a quarter of it left out the time falls by 46 us, without the loaders' conversions not at
 // all.  Lanes with four rows and a quarter of the slots each, which read a quarter of the scales, take 411 us; two numbers a
 // slot, with the largest weight looked at after the exponentials, 557, and once a tile instead of every 32 slots 445.
@@ -603,7 +603,15 @@ __global__ void __launch_bounds__(kThreads<Q8>, 1)
             if (lane >= draft && value_row)
               for (int c = 0; c < LPR; ++c) nan = nan || has_nan(__ldg(reinterpret_cast<const uint4*>(value_row) + c));
           }
-          const float log_v = lg2(fminf(fmaxf(value, 0x1p-64f), 0x1p64f));
+          float log_v = lg2(fminf(fmaxf(value, 0x1p-64f), 0x1p64f));
+          // a slot of zero values?  (as a rule the first 16 codes tell; for all slots by loads of whole rows: 454 us for 390)
+          if (value == kZeroScale && value_row) {
+            bool some = false;
+#pragma unroll 1
+            for (int c = 0; c < LPR && !some; ++c) some = not_zero(__ldg(reinterpret_cast<const uint4*>(value_row) + c));
+            if (!some) log_v = kZeroCounts;
+          }
+          __syncwarp();
           const int sn = t % (2 * C::NS);
           sc.key[sn][lw * 32 + lane] = key;
           sc.value[sn][lw * 32 + lane] = nan ? __int_as_float(0x7fffffff) : log_v;

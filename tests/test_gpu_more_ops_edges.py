@@ -4,9 +4,9 @@ import math
 import pytest
 import torch
 
-from _more_ops import norm_ref, rounded
+from _more_ops import norm_ref, quantised, rounded
 from mixture_experts_ffn_moe_gb300 import build, gbmoe
-from test_gpu_more_ops import BF, F32, I32, close, gen
+from test_gpu_more_ops import BF, F32, FP, I32, attend, close, gen, make_cache, make_q, ref_of
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,53 @@ def test_norm_rope_of_as_many_heads_as_it_takes():
     gbmoe.moe_qk_norm_rope(q, None, torch.zeros(T, dtype=I32, device="cuda"), f, w, None, 1e-6, q_out=q)
     whole = T // many * many
     assert (q[:whole].view(-1, many) == want.view(1, many)).all() and torch.equal(q[whole:], want[:T - whole])
+
+
+# ------------------------------------------------------------------ attention over the cache
+def with_zero_values(lens, counts, D, page, seed, zeros, scale, sink):
+    """A cache of one KV head whose values have the size 448 * scale, but for the slots `zeros`, which hold zeros as the append writes
+    them (scale 1); with `sink` these take 2^13 times the others' share."""
+    side, table = make_cache(lens, counts, 1, D, page, seed, spread=0.0)
+    (kc, ks), (vc, vs) = side
+    base = torch.randn(D, generator=gen(seed))
+    for b, n in enumerate(lens):
+        for s in range(n + counts[b]):
+            at = (int(table[b, s // page]), s % page, 0)
+            strong = sink and zeros(s)
+            key = base / (base @ base) * (13.0 * math.log(2.0) * D ** 0.5) if strong else 0.05 * torch.randn(D, generator=gen(s))
+            c, x = quantised(key[None])
+            kc[at], ks[at] = c[0], x[0]
+            vs[at] = scale
+            if zeros(s):
+                vc[at], vs[at] = 0, 1.0
+    return base, side, table
+
+
+@pytest.mark.parametrize("where,scale", [("sink", 2.0 ** -12), ("all over", 2.0 ** -29), ("all over", 2.0 ** -36), ("run", 2.0 ** -29)])
+@pytest.mark.parametrize("hq,counts", [(4, [1, 1]), (8, [2, 1]), (16, [2, 2]), (16, [8, 9]), (16, [20, 18])])
+@pytest.mark.parametrize("dt,D,page", [(BF, 128, 16), (FP, 64, 5)])
+def test_fp8_attention_over_slots_of_zero_values(dt, D, page, hq, counts, where, scale):
+    """Slots of zero values (scale 1) add nothing and take no bits from the others, much smaller than that: the bound is that of a
+    cache where these slots have a tiny scale, which is the same cache."""
+    lens = [130, 37]
+    zeros = {"sink": lambda s: s == 3, "all over": lambda s: s % 5 == 3, "run": lambda s: s < 20 or 40 < s < 100}[where]
+    base, side, table = with_zero_values(lens, counts, D, page, 60 + D, zeros, scale, where == "sink")
+    q = (base + 0.05 * torch.randn(sum(counts), hq, D, generator=gen(9))).to(dt)
+    (kc, ks), (vc, vs) = side
+    low = torch.where((vc & 127).amax(-1) == 0, torch.full_like(vs, 2.0 ** -40), vs)
+    ref, bound = ref_of(q, ((kc, ks), (vc, low)), table, lens, counts, None, D ** -0.5)
+    got = attend(q, side, table, lens, counts, None)
+    close(got, ref, bound)
+    assert (ref.abs().amax(-1) > 0).all()
+
+
+@pytest.mark.parametrize("hq,counts", [(4, [1, 1]), (16, [20, 18])])
+def test_fp8_attention_over_nothing_but_zero_values(hq, counts):
+    """All of a sequence's values are zero, or only those that a row sees first: zeros, no NaN."""
+    lens, D, page = [300, 37], 64, 16
+    _, side, table = with_zero_values(lens, counts, D, page, 61, lambda s: s < 290, 1.0, False)
+    q = make_q(counts, hq, D, BF, 61)
+    ref, bound = ref_of(q, side, table, lens, counts, None, D ** -0.5)
+    got = attend(q, side, table, lens, counts, None)
+    close(got, ref, bound)
+    assert (got[counts[0]:] == 0).all() and (got[:counts[0]] != 0).any()
