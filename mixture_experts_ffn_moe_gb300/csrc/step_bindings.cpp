@@ -6,6 +6,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -110,6 +111,16 @@ template <typename T> T* ptr(const Tensor& t) { return static_cast<T*>(t.data_pt
 moe_stream_t stream_of(const Tensor& t) {
   return reinterpret_cast<moe_stream_t>(c10::cuda::getCurrentCUDAStream(t.device().index()).stream());
 }
+// The tensors' device need not be the current one: it is while this lives.
+class OnDevice {
+ public:
+  explicit OnDevice(const at::Device& dev) {
+    if (c10::cuda::current_device() != dev.index()) guard_.set_device(dev);
+  }
+
+ private:
+  c10::cuda::OptionalCUDAGuard guard_;
+};
 Tensor new_like(const Tensor& t, at::IntArrayRef shape, at::ScalarType type) { return at::empty(shape, t.options().dtype(type)); }
 
 PyObject* status(moe_status_t s) { return PyLong_FromLong(s); }
@@ -162,6 +173,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& q = tensor(a[0], "q");
     moe_rope_args_t r = rope_args(q, tensor(a[2], "positions"), tensor(a[3], "inv_freq"), a + 4);
     const at::Device dev = q.device();
+    const OnDevice on(dev);
     Tensor q_out = given(a[8]) ? tensor(a[8], "q_out") : new_like(q, q.sizes(), q.scalar_type()), k_out;
     check(q_out, &dev, q.scalar_type(), {q.size(0), q.size(1), q.size(2)}, "q_out", kRows);
     r.q_out = q_out.data_ptr();
@@ -193,6 +205,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor &kc = tensor(a[6], "k_cache"), &vc = tensor(a[7], "v_cache");
     moe_rope_args_t r = rope_args(q, tensor(a[3], "positions"), tensor(a[4], "inv_freq"), a + 8);
     const at::Device dev = q.device();
+    const OnDevice on(dev);
     const at::ScalarType type = q.scalar_type();
     check(k, &dev, type, {q.size(0), -1, q.size(2)}, "k", kRows);
     check(v, &dev, type, {q.size(0), k.size(1), q.size(2)}, "v", kRows);
@@ -234,6 +247,7 @@ PyObject* linear_int4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bool gated = truth(a[3]);
     const int dtype = dtype_code(x, "x", false);
     const at::Device dev = x.device();
+    const OnDevice on(dev);
     check(x, nullptr, x.scalar_type(), {-1, -1}, "x", kRows);
     const int64_t M = x.size(0), K = x.size(1);
     check(w, &dev, at::kByte, {-1, K / 2}, "w", kContiguous);
@@ -266,6 +280,7 @@ PyObject* tree_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     moe_tree_attention_args_t r{};
     r.dtype = dtype_code(q, "q", false);
     const at::Device dev = q.device();
+    const OnDevice on(dev);
     const at::ScalarType type = q.scalar_type();
     check(q, nullptr, type, {-1, -1, -1}, "q", kRows);
     check(kc, &dev, type, {-1, -1, -1, q.size(2)}, "k_cache", kRows);
@@ -327,6 +342,7 @@ PyObject* verify_draft(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int most = integer(a[5]);
     check(target, nullptr, at::kFloat, {-1, -1}, "target_probs", kRows);
     const at::Device dev = target.device();
+    const OnDevice on(dev);
     check(tokens, &dev, at::kInt, {-1}, "tokens", kContiguous);
     check(last, &dev, at::kFloat, {-1}, "last_coins", kContiguous);
     const int64_t N = tokens.size(0), B = last.size(0), V = target.size(1);
@@ -434,7 +450,7 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& q = tensor(a[0], "q");
     moe_qk_norm_rope_args_t r = norm_args(q, tensor(a[2], "positions"), tensor(a[3], "inv_freq"), a[4], a[5], a + 6);
     const at::Device dev = q.device();
-    const c10::cuda::CUDAGuard guard(dev);  // (the tensors' device need not be the current one)
+    const OnDevice on(dev);
     Tensor q_out = given(a[10]) ? tensor(a[10], "q_out") : new_like(q, q.sizes(), q.scalar_type()), k_out;
     check(q_out, &dev, q.scalar_type(), {q.size(0), q.size(1), q.size(2)}, "q_out", kRows);
     r.q_out = q_out.data_ptr();
@@ -466,7 +482,7 @@ PyObject* qk_norm_rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &slots = tensor(a[5], "slots");
     moe_qk_norm_rope_args_t r = norm_args(q, tensor(a[3], "positions"), tensor(a[4], "inv_freq"), a[8], a[9], a + 12);
     const at::Device dev = q.device();
-    const c10::cuda::CUDAGuard guard(dev);  // (the tensors' device need not be the current one)
+    const OnDevice on(dev);
     const at::ScalarType type = q.scalar_type();
     check(k, &dev, type, {q.size(0), -1, q.size(2)}, "k", kRows);
     check(v, &dev, type, {q.size(0), k.size(1), q.size(2)}, "v", kRows);
@@ -515,7 +531,7 @@ PyObject* cache_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::ScalarType type = r.dtype == MOE_DTYPE_BF16 ? at::kBFloat16 : r.dtype == MOE_DTYPE_FP16 ? at::kHalf : at::kFloat;
     if (!kc.is_cuda()) bad("k_cache must be a CUDA tensor");
     const at::Device dev = kc.device();
-    const c10::cuda::CUDAGuard guard(dev);  // (the tensors' device need not be the current one)
+    const OnDevice on(dev);
     check_codes(a[0], dev, {-1, -1, -1, -1}, "k_cache");
     const Tensor& ks = check_scale(a[2], dev, kc, "k_scale");
     check(slots, &dev, at::kInt, {-1}, "slots", kContiguous);
@@ -558,7 +574,7 @@ PyObject* tree_attention_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Device dev = q.device();
     const at::ScalarType type = q.scalar_type();
     check(q, nullptr, type, {-1, -1, -1}, "q", kRows);
-    const c10::cuda::CUDAGuard guard(dev);  // (the tensors' device need not be the current one)
+    const OnDevice on(dev);
     check_codes(a[1], dev, {-1, -1, -1, q.size(2)}, "k_cache");
     check_codes(a[2], dev, {kc.size(0), kc.size(1), kc.size(2), q.size(2)}, "v_cache");
     const Tensor &ks = check_scale(a[3], dev, kc, "k_scale"), &vs = check_scale(a[4], dev, vc, "v_scale");
@@ -614,7 +630,7 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
     r.dtype = dtype_code(logits, "logits", true);
     check(logits, nullptr, logits.scalar_type(), {-1, -1}, "logits", kRows);
     const at::Device dev = logits.device();
-    const c10::cuda::CUDAGuard guard(dev);  // (the tensors' device need not be the current one)
+    const OnDevice on(dev);
     const int64_t R = logits.size(0), V = logits.size(1);
     auto setting = [&](PyObject* o, at::ScalarType type, const char* name) -> void* {
       if (!given(o)) return nullptr;

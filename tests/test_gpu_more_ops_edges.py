@@ -101,3 +101,36 @@ def test_fp8_attention_over_nothing_but_zero_values(hq, counts):
     got = attend(q, side, table, lens, counts, None)
     close(got, ref, bound)
     assert (got[counts[0]:] == 0).all() and (got[:counts[0]] != 0).any()
+
+
+# ------------------------------------------------------------------ devices
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two GPUs")
+def test_calls_run_on_their_tensors_device():
+    """Every call of a decode step, with tensors on a device that is not the current one."""
+    g = gen(70)
+    D, page, V = 64, 16, 500
+    x = torch.randn(2, 6, D, generator=g).to(BF)
+    pos, slots, offs = torch.tensor([0, 3], dtype=I32), torch.tensor([0, 19], dtype=I32), torch.arange(3, dtype=I32)
+    w, s = torch.randint(0, 256, (32, D // 2), generator=g, dtype=torch.uint8), torch.rand(32, 2, generator=g)
+    cache, scale = torch.randn(4, page, 2, D, generator=g), torch.rand(4, page, 2, generator=g) + 0.1
+    logits, coins = torch.randn(4, V, generator=g), torch.rand(4, generator=g)
+
+    def calls(dev):
+        d = [t.to(dev) for t in (x, pos, slots, offs, w, s, cache.to(BF), cache.to(BF), cache.to(torch.float8_e4m3fn),
+                                 cache.to(torch.float8_e4m3fn), scale, scale, logits, coins)]
+        f, table = gbmoe.rope_frequencies(D, device=dev)[0], torch.tensor([[0], [1]], dtype=I32, device=dev)
+        q, k, v = d[0][:, :2], d[0][:, 2:4], d[0][:, 4:]
+        probs = gbmoe.moe_filter_probs(d[12])
+        return [*gbmoe.moe_rope(q, k, d[1], f), gbmoe.moe_rope_append(q, k, v, d[1], f, d[2], d[6], d[7]),
+                gbmoe.moe_linear_int4(q[:, 0], d[4], d[5]), gbmoe.moe_tree_attention(q, d[6], d[7], table, d[1], d[3]),
+                *gbmoe.moe_verify_draft(probs, d[2], d[3], d[13], d[13][:2], 1), *gbmoe.moe_qk_norm_rope(q, k, d[1], f),
+                gbmoe.moe_qk_norm_rope_append(q, k, v, d[1], f, d[2], d[8], d[9], None, None, d[10], d[11]),
+                gbmoe.moe_tree_attention_fp8(q, d[8], d[9], d[10], d[11], table, d[1], d[3]),
+                *gbmoe.moe_cache_read(d[8], d[9], d[10], d[11], d[2]), gbmoe.moe_sample(d[12], d[13]), probs]
+
+    with torch.cuda.device(0):
+        here, there = calls("cuda:0"), calls("cuda:1")
+        torch.cuda.synchronize(1)
+        assert torch.cuda.current_device() == 0
+    for a, b in zip(here, there):
+        assert b.device.index == 1 and torch.equal(a.float().cpu(), b.float().cpu())
