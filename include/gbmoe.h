@@ -743,7 +743,9 @@ moe_status_t moe_tree_attention_fp8(const moe_tree_attention_fp8_args_t* args, v
  * (sum of kept w_i); probs[row, x] = w_x / (sum of kept w_i), 0 for what is not kept, fp32.
  * A temperature of 0 or below, or NaN: the first token of the largest logit alone.
  * Weights count in units of 2^-44, off by 2^-28 of themselves and a unit, and their sums are
- * exact: results do not depend on scheduling.  NaN logits count as -infinity; a row
+ * exact: results do not depend on scheduling.  So a probability below e^-31 of the row's
+ * largest is 0, and those just above it have few bits: their logarithms are not those of an
+ * fp32 softmax.  NaN logits count as -infinity; a row
  * of nothing else gives the token -1 and probabilities of 0.  Tokens of an infinite logit
  * share the row alike; a logit below the largest by more than fp32's range has no weight.
  *   logits   [rows, vocab] of dtype, row stride of at least vocab; vocab <= 524,288

@@ -26,7 +26,8 @@
 // permuted (code_at) such that both patterns are free of bank conflicts.
 //
 // Measured: those 64 sequences (579 MB) in 110 us = 5.3 TB/s; the loads alone, without any product, take 101 to 104 of them,
-// planning, the first loads and the join 8.  One sequence of 65,536 slots 35 us; one of 37 slots 5.0 us.
+// planning, the first loads and the join 8.  One sequence of 65,536 slots 36 us (floor 20); one of 37 slots 5.1 us.  8 KV heads
+// of 64, 64 sequences of those lengths: 64 us (floor 44).
 #include <cuda_runtime.h>
 
 #include "tree_attention.cuh"
@@ -524,8 +525,14 @@ __global__ void __launch_bounds__(kFThreads, F8Cfg<D, RN>::kCtas) tree_fp8_kerne
   }
 }
 
-// How a call is cut, from the host's sizes: the average tree's rows a KV head; more than 64 go to the tcgen05 kernel
-// (16 sequences of 2000 slots, 8 KV heads of 128: 64 rows 51 us in two tiles of 32 here, 77 there).
+// How a call is cut, from the host's sizes: the average tree's rows a KV head; more than 64 go to the tcgen05 kernel.  Measured
+// with 16 sequences of 2000 slots, 8 KV heads, in tiles of 8, 16, 32 rows and on tcgen05, us:
+//   heads of 128:  8 rows 24, 29, 35, 68;  16 rows 30, 30, 37, 68;  32 rows 39, 37, 41, 69;  64 rows 66, 59, 60, 71;
+//                  96 rows 94, 84, 77, 74;  128 rows 116, 101, 98, 77
+//   heads of 64:   8 rows 20, 23, 26, 57;  16 rows 23, 22, 27, 58;  32 rows 30, 26, 28, 58;  64 rows 47, 38, 41, 59;
+//                  96 rows 68, 56, 52, 61;  128 rows 84, 63, 64, 63
+// So tiles of 32 come out level with tiles of 16 between 17 and 64 rows (1 to 9% behind in this shape), and at heads of 64 the
+// border to tcgen05 could lie at 128 rows.
 struct F8Plan { int rows, sides, ranks; bool wide; };
 F8Plan f8_plan(int N, int B, int Hq, int Hkv, int dim, bool adjacent) {
   const long long avg = (static_cast<long long>(N) + B - 1) / B * (Hq / Hkv);
@@ -574,7 +581,8 @@ cudaError_t launch_fp8_typed(const TreeArgs& a, int D, bool wide, int sms, bool 
     err = D == 128 ? launch_fp8_rows<T, 128>(a, sms, s) : launch_fp8_rows<T, 64>(a, sms, s);
   }
   if (err != cudaSuccess || one_tile) return err;  // a unit of one tile is never cut
-  // few rows, so long ones: 8 warps each (one sequence of 65,536 slots, 32 heads: 46 us with one, 40 with 8)
+  // few rows, so long ones: 8 warps each (32 heads, one sequence of 1,000 slots 10.7 us, 12.9 with one warp; 8,000 slots 14, 23;
+  // 65,536 slots 37, 49; 16 sequences of 8,000 slots 59, 61)
   return launch_tree_join(a, kBf16, D, !wide && static_cast<long long>(a.N) * a.Hq <= 4LL * sms, s);
 }
 

@@ -18,8 +18,10 @@
 // rows of a tile where they are needed, a tile ahead, and turn them into fp16 in place, which is exact; the products are those
 // of fp16.  The softmax takes three numbers a slot from shared memory: the key's scale, log2 of the value's, and the power of
 // two that takes that off again.  Two documents of 50,003 to 65,536 slots, 64 nodes, 64 / 4 heads of 128: 390 us = 622 TFLOP/s.
-// There the softmax bounds it: with a quarter of it left out the time falls by 46 us, without the loaders' conversions not at
-// all.  Lanes with four rows and a quarter of the slots each, which read a quarter of the scales, take 411 us; two numbers a
+// There a chain bounds it, not a number of instructions (40% of the issue slots are used): a tile's softmax, the whole of its P,
+// the second product, and the next S, which takes P's place.  With a quarter of the softmax left out the time falls by 46 us, with
+// three quarters by 139, without the loaders' conversions not at all.  Reading the codes back (61 us) and attending to them in
+// 16 bits (246) would take 305 us.  Lanes with four rows and a quarter of the slots each, which read a quarter of the scales, take 411 us; two numbers a
 // slot, with the largest weight looked at after the exponentials, 557, and once a tile instead of every 32 slots 445.
 //
 // CTAs whose row tiles belong to the same cache range (up to 4) walk over it side by side, so that HBM delivers it
