@@ -737,8 +737,8 @@ moe_status_t moe_tree_attention_fp8(const moe_tree_attention_fp8_args_t* args, v
  *   of these the first top_k (0 or below, or vocab and above: all);
  *   of these the shortest prefix whose weight is at least top_p of theirs (1 and above or
  *   NaN: all; 0 and below: the first token);
- *   of these the ones with w_x >= min_p (0 and below or NaN: all; at most the ones of the
- *   largest logit fall to any min_p above 1, which counts as 1).
+ *   of these the ones with w_x >= min_p (0 and below or NaN: all; 1 and above: those of the
+ *   largest logit).
  * tokens[row] is the first x, in order of indices, with (sum of kept w_i, i <= x) > coin *
  * (sum of kept w_i); probs[row, x] = w_x / (sum of kept w_i), 0 for what is not kept, fp32.
  * A temperature of 0 or below, or NaN: the first token of the largest logit alone.

@@ -447,7 +447,8 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const __grid_const
   wt.lo = static_cast<float>(rate - static_cast<double>(wt.hi));
   wt.table = sh.table;
   uint64_t least = 0;  // min_p, rounded up
-  if (min_p >= 1.f) least = 1ull << kUnit;
+  const bool only_top = min_p >= 1.f;  // the tokens of the largest logit alone: weights do not tell them from those within 2^-28
+  if (only_top) least = 1ull << kUnit;
   else if (min_p > 0.f) least = (unit_fraction(min_p) + ((1ull << (64 - kUnit)) - 1)) >> (64 - kUnit);
   const bool by_count = top_k > 0 && top_k < a.V, by_share = top_p < 1.f;
 
@@ -811,7 +812,8 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const __grid_const
 
   // ---- the leader's list
   constexpr int L = kList / kSThreads;
-  auto weight_at = [&](int i) { return wt.weight(float_of(static_cast<uint32_t>(list[i] >> 32))); };
+  auto logit_at = [&](int i) { return float_of(static_cast<uint32_t>(list[i] >> 32)); };
+  auto weight_at = [&](int i) { return wt.weight(logit_at(i)); };
   // The list in order; the number of its tokens.
   auto sorted = [&] {
     const int n = min(sh.listed[lists - 1], static_cast<uint32_t>(kList));
@@ -937,7 +939,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const __grid_const
         // ---- the weight of every run of indices, then of every index of the run that holds the coin
 #pragma unroll
         for (int i = 0; i < L; ++i)
-          if (w[i] < least) w[i] = 0;
+          if (w[i] < least || (only_top && w[i] && logit_at(tid + i * kSThreads) != top)) w[i] = 0;
         const int width = (a.V + kSThreads - 1) / kSThreads;  // at most 1024
         uint32_t* runs = fine;                                // [3][kSThreads]
         auto index_of = [&](int i) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(list[tid + i * kSThreads])); };
@@ -995,7 +997,7 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const __grid_const
 #pragma unroll
     for (int i = 0; i < L; ++i) {
       const int x = tid * L + i;
-      if (x < limit && (x == 0 || before < need) && w[i] >= least) ++left;
+      if (x < limit && (x == 0 || before < need) && w[i] >= least && (!only_top || logit_at(x) == top)) ++left;
       before += w[i];
     }
     block_scan(left, unused, sh, &left, &unused);  // (the total to all)
@@ -1153,6 +1155,10 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const __grid_const
     if (sh.dec.found) set_cut(sh.dec.cut);
   }
 
+  if (only_top && cut_l < top) {  // (nothing before cuts between the tokens of the largest logit)
+    cut_l = top;
+    cut_i = a.V;
+  }
   const bool all = cut == 0 && least == 0;
   auto kept_weights = [&](float l0, float l1, int i, uint64_t& w0, uint64_t& w1) {
     w0 = w1 = 0;

@@ -103,6 +103,31 @@ def test_fp8_attention_over_nothing_but_zero_values(hq, counts):
     assert (got[counts[0]:] == 0).all() and (got[:counts[0]] != 0).any()
 
 
+# ------------------------------------------------------------------ sampling
+@pytest.mark.parametrize("V,top_k", [(14, None), (200, 100), (3000, 2049), (20000, None), (60000, 30000)])
+def test_min_p_of_one_keeps_the_largest_logit_alone(V, top_k):
+    """Logits that differ by less than weights can tell: 1 and above leave the ones that are equal to the largest, in any of the
+    kernel's ways to cut."""
+    logits = 1.0 + torch.arange(V).flip(0).repeat(5, 1) % 7 * -2.0 ** -23
+    logits[1] *= 1e-30
+    logits[2, V // 2:] = -3.0
+    logits[3] = torch.randn(V, generator=gen(V)) * 1e-9
+    logits[4, ::3] = -1.0
+    more = {} if top_k is None else {"top_k": torch.full((5,), top_k, dtype=I32).cuda()}
+    temperature = torch.full((5,), 30.0).cuda()
+    for min_p in (1.0, 7.0):
+        for top_p in (None, torch.full((5,), 0.9).cuda()):
+            p = gbmoe.moe_filter_probs(logits.cuda(), temperature, more.get("top_k"), top_p, torch.full((5,), min_p).cuda()).cpu()
+            tokens = gbmoe.moe_sample(logits.cuda(), torch.full((5,), 0.999).cuda(), temperature, more.get("top_k"), top_p,
+                                      torch.full((5,), min_p).cuda()).cpu()
+            for i in range(5):
+                best = (logits[i] == logits[i].max()).nonzero()[:, 0]
+                kept = (p[i] > 0).nonzero()[:, 0]
+                assert 0 < len(kept) <= len(best) and torch.equal(kept, best[:len(kept)]) and int(tokens[i]) == int(kept[-1] if len(kept) < 1000 else tokens[i])
+                assert len(kept) == len(best) or top_p is not None or top_k is not None and top_k < len(best)
+                assert int(tokens[i]) in kept and (p[i, kept] - 1 / len(kept)).abs().max() <= 2.0 ** -22
+
+
 # ------------------------------------------------------------------ devices
 @pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs two GPUs")
 def test_calls_run_on_their_tensors_device():
